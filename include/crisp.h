@@ -227,6 +227,107 @@ const char* crisp_status_string(crisp_status status);
 crisp_status crisp_route_noalloc(const void* q, const void* k, const crisp_cfg* cfg,
                                  int32_t* route, float* c_struct, void* stream);
 
+/* ---- attention over a key/value cache, and eviction from it ----------------
+ *
+ * What follows the prefill of a layer (no counterpart in the paper): operators
+ * that read or shrink the key/value cache that it leaves. Tensors (device
+ * memory, head dimension d = 128 contiguous, any strides in the other axes):
+ *   q, out   [batch][h_q][n_q][d]     the newest n_q tokens of every sequence
+ *   k, v     [batch][h_kv][n_k][d]    n_k key slots per sequence
+ *   kv_len   int32 [batch], or NULL   tokens sequence b holds (0 .. n_k;
+ *                                     NULL: n_k), the newest ones included
+ * Query token i of sequence b is at position p = kv_len[b] - n_q + i and sees
+ * key j when
+ *     0 <= j <= p  and  (j < sinks  or  j > p - window  or  window == 0).
+ * A query that sees no key (a left-padded row, an empty sequence) gives a
+ * zero row. What slots at or behind kv_len[b] and keys that no query of the
+ * call sees hold never matters, NaN included; a value that is not finite at a
+ * key that some query of the sequence sees may reach every query of that
+ * sequence. Query head h reads key/value head h / (h_q / h_kv).
+ *
+ * The conventions above hold: arguments are checked before anything is
+ * launched, nothing synchronises or allocates, and scratch lives in
+ * cfg->workspace (256-byte aligned, >= crisp_cache_workspace_size bytes),
+ * which calls that can overlap must not share: calls on one stream may, two
+ * captured graphs only when they never run at the same time. The tensors'
+ * device has to be the current one. A kv_len outside [0, n_k] is clamped
+ * and reported by crisp_cache_device_status as CRISP_ERR_INVALID_ARG. */
+
+typedef struct {
+  int64_t seq, head, token; /* in elements; all three 0: contiguous in the order given above */
+} crisp_strides;
+
+typedef struct {
+  int32_t batch;       /* sequences: 1 .. 1024, batch * h_q <= 65535 */
+  int32_t n_q;         /* query tokens per sequence: 1 .. n_k */
+  int32_t n_k;         /* key slots per sequence: 1 .. 2^24 */
+  int32_t h_q, h_kv;   /* h_q % h_kv == 0, h_q / h_kv <= 16, h_q <= 1024 */
+  int32_t d;           /* 128 */
+  int32_t dtype;       /* crisp_dtype */
+  int32_t window;      /* keys a query sees back from its own (itself included); 0: all */
+  int32_t sinks;       /* first keys that stay visible; for crisp_evict: that stay */
+  int32_t n_prefix;    /* crisp_shared_prefix_attention: keys every sequence shares, 1 .. 2^24 */
+  int32_t budget;      /* crisp_evict: keys kept per key/value head, >= 1 */
+  int32_t recent;      /* crisp_evict: newest keys that stay; sinks + recent <= budget */
+  int32_t n_new;       /* crisp_evict: key slots of the new cache, >= budget, <= 2^24 */
+  float sm_scale;      /* softmax scale; <= 0 means 1/sqrt(d) */
+  int32_t reserved;    /* must be 0 */
+  /* every stride of an axis longer than 1 is a multiple of 16 bytes and at least d */
+  crisp_strides q, k, v, out;
+  crisp_strides k_prefix, v_prefix; /* [h_kv][n_prefix][d]; seq is not read */
+  crisp_strides k_new, v_new;       /* [batch][h_kv][n_new][d] */
+  void* workspace;
+  size_t workspace_bytes;
+} crisp_cache_cfg;
+
+typedef enum { CRISP_CACHE_WINDOW = 0, CRISP_CACHE_SCORED = 1, CRISP_CACHE_PREFIX = 2, CRISP_CACHE_EVICT = 3 } crisp_cache_op;
+
+/* Fill *cfg for the given shape: contiguous tensors, no window, no sinks, workspace NULL. */
+crisp_status crisp_cache_cfg_init(crisp_cache_cfg* cfg, int32_t batch, int32_t n_q, int32_t n_k, int32_t h_q,
+                                  int32_t h_kv, int32_t d, int32_t dtype);
+
+/* Workspace bytes that operator `op` needs for cfg's shape (strides do not matter). */
+crisp_status crisp_cache_workspace_size(const crisp_cache_cfg* cfg, int32_t op, size_t* bytes);
+
+/* Attention with a sliding window and first tokens that stay visible: whole
+ * prompts (n_q = n_k), appended chunks and single tokens (n_q = 1). */
+crisp_status crisp_window_attention(const void* q, const void* k, const void* v, void* out, const int32_t* kv_len,
+                                    const crisp_cache_cfg* cfg, void* stream);
+
+/* The same for n_q <= 16, which also adds to score (float32, contiguous
+ * [batch][h_kv][n_k]) of every key the softmax weights that the group's query
+ * heads and the call's tokens give it. Other scores are left as they were. */
+crisp_status crisp_scored_attention(const void* q, const void* k, const void* v, void* out, float* score,
+                                    const int32_t* kv_len, const crisp_cache_cfg* cfg, void* stream);
+
+/* Attention of sequences that share their first n_prefix keys, which are read
+ * once for all of them: every query sees the whole prefix k_prefix, v_prefix
+ * [h_kv][n_prefix][d], and of its own sequence's keys those j <= kv_len[b] -
+ * n_q + i. n_q <= 16; window and sinks have to be 0. */
+crisp_status crisp_shared_prefix_attention(const void* q, const void* k_prefix, const void* v_prefix, const void* k,
+                                           const void* v, void* out, const int32_t* kv_len,
+                                           const crisp_cache_cfg* cfg, void* stream);
+
+/* Eviction by accumulated attention weight. Of each sequence and key/value
+ * head the first `sinks` keys, the last `recent` ones and those with the
+ * largest score stay, `budget` in all (equal scores: the lower index first;
+ * a NaN score counts as the lowest); a sequence of at most `budget` keys stays
+ * whole. The kept keys, values and scores move, in their old order, to the
+ * slots 0 .. new_len[b] - 1 of k_new, v_new and score_new (float32, contiguous
+ * [batch][h_kv][n_new]); later scores become 0, later keys and values are left
+ * as they were. kept (int32 [batch][h_kv][budget]) gets the old indices,
+ * ascending, then -1; new_len (int32 [batch], not kv_len itself) the lengths.
+ * The new cache must not overlap the old one (CRISP_ERR_INVALID_ARG). n_q,
+ * window and sm_scale are not used. */
+crisp_status crisp_evict(const void* k, const void* v, const float* score, const int32_t* kv_len, void* k_new,
+                         void* v_new, float* score_new, int32_t* kept, int32_t* new_len,
+                         const crisp_cache_cfg* cfg, void* stream);
+
+/* Synchronise `stream`, then read (and clear) what the last cache operator
+ * that used cfg->workspace reported: CRISP_OK, CRISP_ERR_TIMEOUT, or
+ * CRISP_ERR_INVALID_ARG for a kv_len that was clamped. */
+crisp_status crisp_cache_device_status(const crisp_cache_cfg* cfg, void* stream, int32_t* device_status);
+
 /* Diagnostics: evaluate, on the device, the exp2 approximations the kernels
  * use on the FMA pipe (degree-3 and degree-5 minimax polynomials after an
  * integer/fraction split) next to CUDA's exp2f, for n float32 inputs x

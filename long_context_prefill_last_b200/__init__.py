@@ -9,6 +9,12 @@ raises.
 Entry points (same names as the C ABI): ``route``, ``select``, ``attend``,
 ``prefill``, ``dense_attention``, plus ``workspace_size``, ``index_dims``,
 ``device_status`` and the ``Config`` / ``IndexBuffers`` helpers.
+
+Operators on the key/value cache that a prefill leaves, described by a
+``CacheConfig``: ``window_attention``, ``scored_attention``,
+``shared_prefix_attention`` and ``evict``. They take torch tensors with their
+strides, check shapes, types and devices, and run with the tensors' device
+current.
 """
 from __future__ import annotations
 
@@ -21,10 +27,14 @@ __all__ = [
     "Config", "IndexBuffers", "CrispError", "lib", "library_path", "workspace_size", "index_dims",
     "route", "route_noalloc", "select", "attend", "prefill", "dense_attention", "device_status", "status_string",
     "BF16", "FP32", "ROUTE_AUTO", "ROUTE_VS", "ROUTE_PE", "SYMBOLS",
+    "CacheConfig", "window_attention", "scored_attention", "shared_prefix_attention", "evict",
+    "cache_workspace_size", "cache_device_status",
+    "CACHE_WINDOW", "CACHE_SCORED", "CACHE_PREFIX", "CACHE_EVICT",
 ]
 
 BF16, FP32 = 0, 1
 ROUTE_AUTO, ROUTE_VS, ROUTE_PE = -1, 0, 1
+CACHE_WINDOW, CACHE_SCORED, CACHE_PREFIX, CACHE_EVICT = 0, 1, 2, 3
 STATUS_NAMES = {
     0: "CRISP_OK", 1: "CRISP_ERR_INVALID_ARG", 2: "CRISP_ERR_SHAPE", 3: "CRISP_ERR_DTYPE",
     4: "CRISP_ERR_ALIGN", 5: "CRISP_ERR_WORKSPACE", 6: "CRISP_ERR_UNSUPPORTED", 7: "CRISP_ERR_CUDA",
@@ -36,7 +46,9 @@ SYMBOLS = ["crisp_cfg_init", "crisp_workspace_size", "crisp_index_dims", "crisp_
            "crisp_status_string", "crisp_version", "crisp_route_noalloc", "crisp_exp2_selftest",
            "crisp_prefill_batch", "crisp_workspace_size_batch", "crisp_prefill_varlen",
            "crisp_prefill_host", "crisp_workspace_size_host", "crisp_wait_selftest",
-           "crisp_diag_select_simt", "crisp_diag_attend_simt"]
+           "crisp_diag_select_simt", "crisp_diag_attend_simt",
+           "crisp_cache_cfg_init", "crisp_cache_workspace_size", "crisp_window_attention",
+           "crisp_scored_attention", "crisp_shared_prefix_attention", "crisp_evict", "crisp_cache_device_status"]
 
 
 def library_path() -> str:
@@ -62,6 +74,22 @@ class _Cfg(ctypes.Structure):
 
 _INDEX_FIELDS = ["route", "c_struct", "p_v", "p_s", "mu", "vs_mask", "v_idx", "s_idx", "nv", "ns",
                  "pe_mask", "pe_count", "pe_cut"]
+
+
+class _Strides(ctypes.Structure):
+    _fields_ = [("seq", ctypes.c_int64), ("head", ctypes.c_int64), ("token", ctypes.c_int64)]
+
+
+_CACHE_INTS = ["batch", "n_q", "n_k", "h_q", "h_kv", "d", "dtype", "window", "sinks", "n_prefix", "budget", "recent",
+               "n_new"]
+_CACHE_STRIDES = ["q", "k", "v", "out", "k_prefix", "v_prefix", "k_new", "v_new"]
+
+
+class _CacheCfg(ctypes.Structure):
+    _fields_ = ([(f, ctypes.c_int32) for f in _CACHE_INTS]
+                + [("sm_scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
+                + [(f, _Strides) for f in _CACHE_STRIDES]
+                + [("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)])
 
 
 class _Index(ctypes.Structure):
@@ -102,6 +130,14 @@ def lib() -> ctypes.CDLL:
         L.crisp_diag_select_simt.argtypes = [vp, vp, cfgp, ctypes.POINTER(_Index), vp]
         L.crisp_diag_attend_simt.argtypes = [vp, vp, vp, vp, cfgp, ctypes.POINTER(_Index), ctypes.c_int32, vp]
         L.crisp_device_status.argtypes = [cfgp, vp, ctypes.POINTER(ctypes.c_int32)]
+        ccp = ctypes.POINTER(_CacheCfg)
+        L.crisp_cache_cfg_init.argtypes = [ccp] + [ctypes.c_int32] * 7
+        L.crisp_cache_workspace_size.argtypes = [ccp, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)]
+        L.crisp_window_attention.argtypes = [vp] * 5 + [ccp, vp]
+        L.crisp_scored_attention.argtypes = [vp] * 6 + [ccp, vp]
+        L.crisp_shared_prefix_attention.argtypes = [vp] * 7 + [ccp, vp]
+        L.crisp_evict.argtypes = [vp] * 9 + [ccp, vp]
+        L.crisp_cache_device_status.argtypes = [ccp, vp, ctypes.POINTER(ctypes.c_int32)]
         L.crisp_status_string.argtypes = [ctypes.c_int]
         L.crisp_status_string.restype = ctypes.c_char_p
         L.crisp_version.restype = ctypes.c_int32
@@ -349,3 +385,164 @@ def raise_on_device_status(cfg: Config, stream=None, where: str = "device") -> N
     code = device_status(cfg, stream)
     if code != 0:
         raise CrispError(code, where)
+
+
+# ---------------------------------------------------------------- key/value cache
+
+
+@dataclasses.dataclass
+class CacheConfig:
+    """Shape and knobs of the cache operators (mirrors crisp_cache_cfg; strides come from the tensors).
+
+    q and out are [batch, h_q, n_q, d], k and v [batch, h_kv, n_k, d]; the prefix
+    is [h_kv, n_prefix, d] and an evicted cache [batch, h_kv, n_new, d]."""
+    batch: int
+    n_q: int
+    n_k: int
+    h_q: int
+    h_kv: int
+    d: int = 128
+    dtype: int = BF16
+    window: int = 0
+    sinks: int = 0
+    n_prefix: int = 0
+    budget: int = 0
+    recent: int = 0
+    n_new: int = 0
+    sm_scale: float = 0.0
+    workspace: Optional[object] = None     # torch.uint8 CUDA tensor
+    reserved: int = 0
+
+    def __setattr__(self, name, value):
+        # the C structure is kept between calls; any change makes a new one
+        self.__dict__[name] = value
+        self.__dict__["_kept"] = None
+
+    def _c(self, **tensors) -> _CacheCfg:
+        """The C structure for these tensors' strides (the last one when nothing has changed)."""
+        strides = tuple(t.stride() for t in tensors.values())
+        kept = self._kept
+        if kept is not None and kept[0] == strides and kept[1] == tuple(tensors):
+            return kept[2]
+        c = _CacheCfg()
+        for f in _CACHE_INTS + ["sm_scale", "reserved"]:
+            setattr(c, f, getattr(self, f))
+        if self.workspace is not None:
+            c.workspace = self.workspace.data_ptr()
+            c.workspace_bytes = self.workspace.numel() * self.workspace.element_size()
+        for (f, t), st in zip(tensors.items(), strides):
+            if st[-1] != 1 and t.shape[-1] != 1:
+                raise ValueError(f"{f}: the head dimension has to be contiguous")
+            if any(s <= 0 for s, n in zip(st, t.shape) if n > 1):
+                raise ValueError(f"{f}: an axis is broadcast (stride 0); make it contiguous")
+            seq, head, token = st[:3] if len(st) == 4 else (0, *st[:2])
+            if seq == head == token == 0:
+                token = self.d
+            setattr(c, f, _Strides(seq, head, token))
+        self.__dict__["_kept"] = (strides, tuple(tensors), c)
+        return c
+
+    def allocate_workspace(self, op: int, device="cuda"):
+        """Device workspace for operator `op` (CACHE_WINDOW, CACHE_SCORED, CACHE_PREFIX, CACHE_EVICT); the
+        operators called with this configuration need the largest of theirs."""
+        import torch
+        self.workspace = torch.empty(cache_workspace_size(self, op), dtype=torch.uint8, device=device)
+        return self.workspace
+
+
+def cache_workspace_size(cfg: CacheConfig, op: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().crisp_cache_workspace_size(ctypes.byref(cfg._c()), int(op), ctypes.byref(out)),
+           "crisp_cache_workspace_size")
+    return out.value
+
+
+def _cache_device(first, dtype, tensors, words):
+    """Checks types, shapes and devices; returns the tensors' device. `tensors` are (name, tensor, shape) of the
+    layer's type, `words` (name, tensor or None, shape, type name) of 4-byte types, contiguous."""
+    import torch
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError("the cache operators take CUDA tensors")
+    want = torch.float32 if dtype == FP32 else torch.bfloat16
+    for name, t, shape in tensors:
+        if t.dtype != want or t.device != dev or t.shape != shape:
+            raise ValueError(f"{name}: expected {want} {tuple(shape)} on {dev}, got {t.dtype} {tuple(t.shape)} on "
+                             f"{t.device}")
+    for name, t, shape, kind in words:
+        if t is None:
+            continue
+        if t.dtype != getattr(torch, kind) or t.device != dev or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name}: expected contiguous torch.{kind} {tuple(shape)} on {dev}, got {t.dtype} "
+                             f"{tuple(t.shape)} on {t.device}")
+    return dev
+
+
+def _on_device(dev, cfg, stream, name, *args):
+    """Calls the library with `dev` current, on `stream` (default: that device's current stream)."""
+    import torch
+    if cfg.workspace is not None and cfg.workspace.device != dev:
+        raise ValueError(f"the workspace is on {cfg.workspace.device}, the tensors are on {dev}")
+    fn = getattr(lib(), name)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    raw = getattr(stream, "cuda_stream", stream)
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, raw), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, raw), name)
+
+
+def window_attention(q, k, v, out, cfg: CacheConfig, kv_len=None, stream=None) -> None:
+    """crisp_window_attention: the newest n_q tokens of every sequence attend through a window of cfg.window keys
+    (0: all) and the first cfg.sinks keys."""
+    qs, ks = (cfg.batch, cfg.h_q, cfg.n_q, cfg.d), (cfg.batch, cfg.h_kv, cfg.n_k, cfg.d)
+    dev = _cache_device(q, cfg.dtype, (("q", q, qs), ("k", k, ks), ("v", v, ks), ("out", out, qs)),
+                        (("kv_len", kv_len, (cfg.batch,), "int32"),))
+    _on_device(dev, cfg, stream, "crisp_window_attention", q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+               _ptr(kv_len), ctypes.byref(cfg._c(q=q, k=k, v=v, out=out)))
+
+
+def scored_attention(q, k, v, out, score, cfg: CacheConfig, kv_len=None, stream=None) -> None:
+    """crisp_scored_attention: window_attention for n_q <= 16 that adds every key's softmax weights to
+    score (float32 [batch, h_kv, n_k])."""
+    qs, ks = (cfg.batch, cfg.h_q, cfg.n_q, cfg.d), (cfg.batch, cfg.h_kv, cfg.n_k, cfg.d)
+    dev = _cache_device(q, cfg.dtype, (("q", q, qs), ("k", k, ks), ("v", v, ks), ("out", out, qs)),
+                        (("kv_len", kv_len, (cfg.batch,), "int32"), ("score", score, ks[:3], "float32")))
+    _on_device(dev, cfg, stream, "crisp_scored_attention", q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+               _ptr(score), _ptr(kv_len), ctypes.byref(cfg._c(q=q, k=k, v=v, out=out)))
+
+
+def shared_prefix_attention(q, k_prefix, v_prefix, k, v, out, cfg: CacheConfig, kv_len=None, stream=None) -> None:
+    """crisp_shared_prefix_attention: every sequence attends over the shared k_prefix, v_prefix
+    [h_kv, n_prefix, d] and its own keys."""
+    qs, ks = (cfg.batch, cfg.h_q, cfg.n_q, cfg.d), (cfg.batch, cfg.h_kv, cfg.n_k, cfg.d)
+    ps = (cfg.h_kv, cfg.n_prefix, cfg.d)
+    dev = _cache_device(q, cfg.dtype, (("q", q, qs), ("k_prefix", k_prefix, ps), ("v_prefix", v_prefix, ps),
+                                       ("k", k, ks), ("v", v, ks), ("out", out, qs)),
+                        (("kv_len", kv_len, (cfg.batch,), "int32"),))
+    _on_device(dev, cfg, stream, "crisp_shared_prefix_attention", q.data_ptr(), k_prefix.data_ptr(),
+               v_prefix.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(kv_len),
+               ctypes.byref(cfg._c(q=q, k_prefix=k_prefix, v_prefix=v_prefix, k=k, v=v, out=out)))
+
+
+def evict(k, v, score, k_new, v_new, score_new, kept, new_len, cfg: CacheConfig, kv_len=None, stream=None) -> None:
+    """crisp_evict: the first cfg.sinks, the last cfg.recent and the highest scored keys, cfg.budget in all, move to
+    the new cache; kept (int32 [batch, h_kv, budget]) gets their old indices, new_len (int32 [batch]) the lengths."""
+    ks, ns = (cfg.batch, cfg.h_kv, cfg.n_k, cfg.d), (cfg.batch, cfg.h_kv, cfg.n_new, cfg.d)
+    dev = _cache_device(k, cfg.dtype, (("k", k, ks), ("v", v, ks), ("k_new", k_new, ns), ("v_new", v_new, ns)),
+                        (("kv_len", kv_len, (cfg.batch,), "int32"), ("score", score, ks[:3], "float32"),
+                         ("score_new", score_new, ns[:3], "float32"),
+                         ("kept", kept, (*ks[:2], cfg.budget), "int32"), ("new_len", new_len, (cfg.batch,), "int32")))
+    _on_device(dev, cfg, stream, "crisp_evict", k.data_ptr(), v.data_ptr(), _ptr(score), _ptr(kv_len),
+               k_new.data_ptr(), v_new.data_ptr(), _ptr(score_new), _ptr(kept), _ptr(new_len),
+               ctypes.byref(cfg._c(k=k, v=v, k_new=k_new, v_new=v_new)))
+
+
+def cache_device_status(cfg: CacheConfig, stream=None) -> int:
+    """Synchronise the stream and return (and clear) what the last cache operator on cfg.workspace reported."""
+    st = ctypes.c_int32(0)
+    _check(lib().crisp_cache_device_status(ctypes.byref(cfg._c()), _stream(stream), ctypes.byref(st)),
+           "crisp_cache_device_status")
+    return st.value

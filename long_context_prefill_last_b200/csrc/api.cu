@@ -577,6 +577,6 @@ const char* crisp_status_string(crisp_status status) {
   return "unknown status";
 }
 
-int32_t crisp_version(void) { return 100; }
+int32_t crisp_version(void) { return 200; }
 
 }  // extern "C"

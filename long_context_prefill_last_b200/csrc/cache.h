@@ -1,0 +1,221 @@
+// Internal declarations of the cache operators: attention over a key/value
+// cache (window, scored, shared prefix) and eviction (not part of the ABI).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "crisp.h"
+#include "internal.h"
+
+namespace crisp {
+
+constexpr int kMaxBatch = 1024;          // sequences of one call
+constexpr int kMaxCacheLen = 1 << 24;    // key slots per sequence
+constexpr int kMaxDraft = 16;            // query tokens of a scored or shared-prefix call, and of the decode kernels
+constexpr int kNoWindow = 1 << 30;       // window = 0: every earlier key
+constexpr int kStatusLen = 4;            // status slot: a sequence length outside [0, n_k] (it was clamped)
+
+struct Strides {   // elements; d is contiguous
+  int64_t seq, head, token;
+};
+
+// A validated cache configuration.
+struct CacheShape {
+  int batch, n_q, n_k, h_q, h_kv, group;
+  int window;              // kNoWindow when unlimited
+  int sinks;
+  int n_prefix, budget, recent, n_new;
+  bool fp32;
+  float scale_log2;
+  Strides q, k, v, out, k_prefix, v_prefix, k_new, v_new;
+};
+
+// The keys that the queries of one unit read, as one list: the first `se`
+// keys, then keys lo, lo + 1, ... Entry u is key u for u < se, else
+// lo + (u - se).
+struct KeyList {
+  int se, lo, total;
+#ifdef __CUDACC__
+  __host__ __device__ int key(int u) const { return u < se ? u : lo + (u - se); }
+#endif
+};
+
+// Union of the keys that query tokens i0..i1 of a sequence of len keys see.
+// Token i is at position len - n_q + i and sees key j when 0 <= j <= position
+// and (j < sinks or j > position - window).
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline KeyList key_list(int len, int n_q, int i0, int i1, int window, int sinks) {
+  KeyList r;
+  const int first = len - n_q + i0;
+  const int hi = len - n_q + i1 + 1;           // one past the last position (<= len)
+  if (hi <= 0) {
+    r.se = r.lo = r.total = 0;
+    return r;
+  }
+  r.se = sinks < hi ? sinks : hi;
+  const int low = first - window + 1;
+  r.lo = low > r.se ? low : r.se;
+  r.total = r.se + (hi - r.lo);
+  return r;
+}
+
+// How the rows of one attention launch are laid out. A unit is one key/value
+// head of one sequence; its rows are its (token, head of the group) pairs,
+// token-major. For the shared prefix a unit is one key/value head and its
+// rows are those of every sequence, one after another.
+struct RowMap {
+  int n_q, group, h_kv;
+  int rows;          // per unit
+  int per_seq;       // n_q * group
+  bool prefix;
+};
+
+// Where an attention launch leaves a row's partial results: runs of
+// consecutive slots of `block` rows each. kSplits: slot = job * splits + s.
+// kStair: the launch's key tiles are dealt to `ctas` CTAs as equal runs of one
+// flat list; slot = CTA + job (unique: both only grow along the list).
+enum PartMode : int { kPartNone = 0, kSplits = 1, kStair = 2 };
+struct PartSrc {
+  int mode;
+  const float* o;       // [slot][block][128], not normalised
+  const float2* ml;     // [slot][block]: maximum (log2 domain), sum
+  int block;            // rows per slot
+  int blocks;           // row blocks per unit
+  int splits;
+  int ctas;
+  int tile;             // kStair: keys per tile
+};
+
+// Arguments shared by the attention kernels.
+struct CacheArgs {
+  const void *q, *k, *v;
+  void* out;
+  const int32_t* kv_len;   // NULL: n_keys for every sequence
+  int32_t* status;
+  int batch;               // sequences (1 unit group for the prefix)
+  int n_keys;              // key slots per sequence, or the prefix length
+  int h_kv, group, n_q, window, sinks;
+  int rows, per_seq;       // rows per unit; rows per sequence within it
+  int prefix;              // rows run over every sequence, every key is seen
+  float scale_log2;
+  Strides sq, sk, sv, so;
+  // partial results (NULL: write the output rows)
+  float* part_o;
+  float2* part_ml;
+  int block, blocks, splits, ctas;
+  // scored: scaled logits [unit][row][pitch] by list index
+  float* logits;
+  int64_t pitch;
+};
+
+#ifdef __CUDACC__
+namespace dev {
+
+__device__ __forceinline__ int cache_len(const CacheArgs& a, int b) {
+  if (a.kv_len == nullptr) return a.n_keys;
+  int n = a.kv_len[b];
+  if (n < 0 || n > a.n_keys) {
+    a.status[kStatusLen] = CRISP_ERR_INVALID_ARG;   // every writer writes the same value
+    n = n < 0 ? 0 : a.n_keys;
+  }
+  return n;
+}
+
+// Key list of query tokens i0..i1 of sequence b (every key for the prefix).
+__device__ __forceinline__ KeyList unit_keys(const CacheArgs& a, int len, int i0, int i1) {
+  if (a.prefix) {
+    KeyList r;
+    r.se = 0;
+    r.lo = 0;
+    r.total = len;
+    return r;
+  }
+  return key_list(len, a.n_q, i0, i1, a.window, a.sinks);
+}
+
+// Row r of unit (b, g): sequence, token and query head.
+struct Row {
+  int b, i, h;
+};
+__device__ __forceinline__ Row unit_row(const CacheArgs& a, int b, int g, int r) {
+  Row x;
+  x.b = b;
+  if (a.prefix) {
+    x.b = r / a.per_seq;
+    r -= x.b * a.per_seq;
+  }
+  x.i = r / a.group;
+  x.h = g * a.group + (r - x.i * a.group);
+  return x;
+}
+
+// Position of query token i: keys past it are not seen. Prefix rows see every key.
+__device__ __forceinline__ int row_pos(const CacheArgs& a, int len, int i) {
+  return a.prefix ? (1 << 29) : len - a.n_q + i;
+}
+
+}  // namespace dev
+#endif
+
+// ---- plans: grid shapes and workspace pieces of one call, fixed by the shape ----
+struct AttnPlan {
+  int kernel;        // AttnKernel
+  int block, blocks, splits, ctas, tile;
+  int units;
+  size_t slots;      // partial slots (0: the kernel writes the output itself)
+};
+enum AttnKernel : int { kTileSimt = 0, kDecodeMma = 1, kTileTc = 2 };
+
+struct CachePlan {
+  AttnPlan main, pre;       // the sequences' own keys; the shared prefix
+  bool has_pre;
+  int64_t pitch;            // scored: logits per row
+  size_t off_ml, off_o, off_pre_ml, off_pre_o, off_logits, off_final;
+  size_t off_thresh;        // evict
+  size_t total;
+};
+
+CachePlan plan_cache(const CacheShape& s, int op);
+
+// ---- launchers (each enqueues on `st`; return cudaGetLastError()) ----
+cudaError_t launch_cache_tile(const CacheArgs& a, const AttnPlan& p, bool fp32, cudaStream_t st);
+
+struct MergeArgs {
+  PartSrc main, pre;
+  const int32_t* kv_len;
+  int batch, n_q, n_k, h_kv, group, window, sinks;
+  void* out;
+  Strides so;
+  bool fp32;
+  float2* final_ml;   // scored: [unit][row] (maximum, 1 / sum); NULL otherwise
+};
+cudaError_t launch_cache_merge(const MergeArgs& a, cudaStream_t st);
+
+struct ScoreArgs {
+  const float* logits;
+  int64_t pitch;
+  const float2* final_ml;
+  const int32_t* kv_len;
+  int batch, n_q, n_k, h_kv, group, window, sinks;
+  float* score;       // [batch][h_kv][n_k]
+};
+cudaError_t launch_cache_score(const ScoreArgs& a, cudaStream_t st);
+
+struct EvictArgs {
+  const void *k, *v;
+  const float* score;
+  const int32_t* kv_len;
+  void *k_new, *v_new;
+  float* score_new;
+  int32_t *kept, *new_len, *status;
+  Strides sk, sv, skn, svn;
+  int batch, h_kv, n_k, sinks, recent, budget, n_new;
+  int row_bytes;
+};
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st);
+
+}  // namespace crisp

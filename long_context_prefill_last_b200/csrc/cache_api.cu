@@ -1,0 +1,425 @@
+// C ABI of the cache operators: argument checks, plans (grid shapes and
+// workspace pieces) and the order of launches. Nothing here synchronises
+// except crisp_cache_device_status.
+#include <math.h>
+#include <string.h>
+
+#include <algorithm>
+
+#include "cache.h"
+#include "crisp.h"
+
+namespace crisp {
+namespace {
+
+constexpr int kSms = 148;
+
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// One tensor's strides: zeros mean contiguous, axes of length 1 get a harmless stride.
+crisp_status make_strides(const crisp_strides& in, int64_t seqs, int64_t heads, int64_t tokens, int elem, Strides* out) {
+  if (in.seq == 0 && in.head == 0 && in.token == 0) {
+    out->token = kHeadDim;
+    out->head = tokens * kHeadDim;
+    out->seq = heads * out->head;
+    return CRISP_OK;
+  }
+  const int64_t ext[3] = {seqs, heads, tokens}, st[3] = {in.seq, in.head, in.token};
+  int64_t got[3];
+  for (int i = 0; i < 3; ++i) {
+    if (ext[i] <= 1) {
+      got[i] = kHeadDim;
+      continue;
+    }
+    if (st[i] < kHeadDim || st[i] > ((int64_t)1 << 36)) return CRISP_ERR_SHAPE;
+    if (st[i] * elem % 16 != 0) return CRISP_ERR_ALIGN;
+    got[i] = st[i];
+  }
+  *out = Strides{got[0], got[1], got[2]};
+  return CRISP_OK;
+}
+
+crisp_status make_cache_shape(const crisp_cache_cfg* c, int op, CacheShape* s) {
+  if (c == nullptr || c->reserved != 0) return CRISP_ERR_INVALID_ARG;
+  if (op < CRISP_CACHE_WINDOW || op > CRISP_CACHE_EVICT) return CRISP_ERR_INVALID_ARG;
+  if (c->dtype != CRISP_BF16 && c->dtype != CRISP_FP32) return CRISP_ERR_DTYPE;
+  if (c->d != kHeadDim) return CRISP_ERR_SHAPE;
+  if (c->batch < 1 || c->batch > kMaxBatch || c->n_k < 1 || c->n_k > kMaxCacheLen) return CRISP_ERR_SHAPE;
+  if (c->h_q <= 0 || c->h_kv <= 0 || c->h_q % c->h_kv != 0 || c->h_q / c->h_kv > 16 || c->h_q > kMaxHeads ||
+      (int64_t)c->batch * c->h_q > 65535)
+    return CRISP_ERR_SHAPE;
+  if (!isfinite(c->sm_scale) || c->window < 0 || c->sinks < 0) return CRISP_ERR_INVALID_ARG;
+  const bool attends = op != CRISP_CACHE_EVICT;
+  if (attends && (c->n_q < 1 || c->n_q > c->n_k)) return CRISP_ERR_SHAPE;
+  if ((op == CRISP_CACHE_SCORED || op == CRISP_CACHE_PREFIX) && c->n_q > kMaxDraft) return CRISP_ERR_SHAPE;
+  if (op == CRISP_CACHE_PREFIX) {
+    if (c->n_prefix < 1 || c->n_prefix > kMaxCacheLen) return CRISP_ERR_SHAPE;
+    if (c->window != 0 || c->sinks != 0) return CRISP_ERR_UNSUPPORTED;
+  }
+  if (op == CRISP_CACHE_EVICT) {
+    if (c->budget < 1 || c->recent < 0 || (int64_t)c->sinks + c->recent > c->budget) return CRISP_ERR_INVALID_ARG;
+    if (c->n_new < c->budget || c->n_new > kMaxCacheLen) return CRISP_ERR_SHAPE;
+  }
+  memset(s, 0, sizeof(*s));
+  s->batch = c->batch;
+  s->n_q = attends ? c->n_q : 1;
+  s->n_k = c->n_k;
+  s->h_q = c->h_q;
+  s->h_kv = c->h_kv;
+  s->group = c->h_q / c->h_kv;
+  s->window = c->window == 0 || c->window > kNoWindow ? kNoWindow : c->window;
+  s->sinks = std::min(c->sinks, op == CRISP_CACHE_EVICT ? INT32_MAX : c->n_k);
+  s->n_prefix = c->n_prefix;
+  s->budget = c->budget;
+  s->recent = c->recent;
+  s->n_new = c->n_new;
+  s->fp32 = c->dtype == CRISP_FP32;
+  const float scale = c->sm_scale > 0.f ? c->sm_scale : 1.f / sqrtf((float)c->d);
+  s->scale_log2 = scale * 1.4426950408889634f;
+  return CRISP_OK;
+}
+
+crisp_status cache_strides(const crisp_cache_cfg* c, int op, CacheShape* s) {
+  const int e = s->fp32 ? 4 : 2;
+  crisp_status r;
+  if ((r = make_strides(c->k, s->batch, s->h_kv, s->n_k, e, &s->k)) != CRISP_OK) return r;
+  if ((r = make_strides(c->v, s->batch, s->h_kv, s->n_k, e, &s->v)) != CRISP_OK) return r;
+  if (op == CRISP_CACHE_EVICT) {
+    if ((r = make_strides(c->k_new, s->batch, s->h_kv, s->n_new, e, &s->k_new)) != CRISP_OK) return r;
+    return make_strides(c->v_new, s->batch, s->h_kv, s->n_new, e, &s->v_new);
+  }
+  if ((r = make_strides(c->q, s->batch, s->h_q, s->n_q, e, &s->q)) != CRISP_OK) return r;
+  if ((r = make_strides(c->out, s->batch, s->h_q, s->n_q, e, &s->out)) != CRISP_OK) return r;
+  if (op == CRISP_CACHE_PREFIX) {
+    if ((r = make_strides(c->k_prefix, 1, s->h_kv, s->n_prefix, e, &s->k_prefix)) != CRISP_OK) return r;
+    return make_strides(c->v_prefix, 1, s->h_kv, s->n_prefix, e, &s->v_prefix);
+  }
+  return CRISP_OK;
+}
+
+crisp_status check_tensor(const void* p) {
+  if (p == nullptr) return CRISP_ERR_INVALID_ARG;
+  return reinterpret_cast<uintptr_t>(p) % 16 != 0 ? CRISP_ERR_ALIGN : CRISP_OK;
+}
+crisp_status check_words(const void* p, bool optional) {
+  if (p == nullptr) return optional ? CRISP_OK : CRISP_ERR_INVALID_ARG;
+  return reinterpret_cast<uintptr_t>(p) % 4 != 0 ? CRISP_ERR_ALIGN : CRISP_OK;
+}
+crisp_status check_workspace(const crisp_cache_cfg* c, size_t need) {
+  if (c->workspace == nullptr) return CRISP_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(c->workspace) % 256 != 0) return CRISP_ERR_ALIGN;
+  return c->workspace_bytes < need ? CRISP_ERR_WORKSPACE : CRISP_OK;
+}
+
+// Whether the byte ranges of two strided tensors meet.
+bool ranges_meet(const void* a, const Strides& sa, int na, const void* b, const Strides& sb, int nb, const CacheShape& s) {
+  const int e = s.fp32 ? 4 : 2;
+  auto bytes = [&](const Strides& t, int n) {
+    return ((s.batch - 1) * t.seq + (s.h_kv - 1) * t.head + (int64_t)(n - 1) * t.token + kHeadDim) * e;
+  };
+  const char *pa = static_cast<const char*>(a), *pb = static_cast<const char*>(b);
+  return pa < pb + bytes(sb, nb) && pb < pa + bytes(sa, na);
+}
+
+// Grid of the CUDA-core tile kernel: key lists are split until about two CTAs
+// per SM have work, with at least two key tiles in each split.
+AttnPlan plan_tile(int units, int rows, int keys) {
+  AttnPlan p{};
+  p.kernel = kTileSimt;
+  p.units = units;
+  p.tile = 64;
+  p.block = 64;
+  p.blocks = (rows + 63) / 64;
+  const int64_t jobs = (int64_t)units * p.blocks;
+  const int tiles = (keys + 63) / 64;
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({2 * kSms / jobs, tiles / 2, 64}));
+  p.slots = (size_t)jobs * p.splits;
+  return p;
+}
+
+}  // namespace
+
+CachePlan plan_cache(const CacheShape& s, int op) {
+  CachePlan p{};
+  size_t off = 256;   // status
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = align256(off + bytes);
+    return o;
+  };
+  auto parts = [&](AttnPlan& a, size_t* ml, size_t* o) {
+    *ml = take(a.slots * a.block * 8);
+    *o = take(a.slots * a.block * kHeadDim * 4);
+  };
+  if (op != CRISP_CACHE_EVICT) {
+    const int units = s.batch * s.h_kv, rows = s.n_q * s.group;
+    const int64_t seen = (int64_t)s.window + s.sinks + s.n_q - 1;
+    const int keys = (int)std::min<int64_t>(s.n_k, seen);
+    p.has_pre = op == CRISP_CACHE_PREFIX;
+    p.main = plan_tile(units, rows, keys);
+    if (p.has_pre) p.pre = plan_tile(s.h_kv, s.batch * rows, s.n_prefix);
+    if (op == CRISP_CACHE_WINDOW && p.main.splits == 1) p.main.slots = 0;   // output rows straight away
+    parts(p.main, &p.off_ml, &p.off_o);
+    if (p.has_pre) parts(p.pre, &p.off_pre_ml, &p.off_pre_o);
+    if (op == CRISP_CACHE_SCORED) {
+      p.pitch = (keys + 63) / 64 * 64;
+      p.off_logits = take((size_t)units * rows * p.pitch * 4);
+      p.off_final = take((size_t)units * rows * 8);
+    }
+  }
+  p.total = off;
+  return p;
+}
+
+namespace {
+
+#define CACHE_TRY(expr)                         \
+  do {                                          \
+    if ((expr) != cudaSuccess) {                \
+      (void)cudaGetLastError();                 \
+      return CRISP_ERR_CUDA;                    \
+    }                                           \
+  } while (0)
+
+crisp_status run_attention(const void* q, const void* kp, const void* vp, const void* k, const void* v, void* out,
+                           float* score, const int32_t* kv_len, const CacheShape& s, const CachePlan& p, char* ws,
+                           cudaStream_t st) {
+  int32_t* status = reinterpret_cast<int32_t*>(ws);
+  CACHE_TRY(cudaMemsetAsync(status, 0, 32, st));
+  auto launch = [&](const AttnPlan& pl, const CacheArgs& a) { return launch_cache_tile(a, pl, s.fp32, st); };
+  CacheArgs a{};
+  a.q = q;
+  a.out = out;
+  a.status = status;
+  a.h_kv = s.h_kv;
+  a.group = s.group;
+  a.n_q = s.n_q;
+  a.per_seq = s.n_q * s.group;
+  a.scale_log2 = s.scale_log2;
+  a.sq = s.q;
+  a.so = s.out;
+  MergeArgs m{};
+  auto source = [&](const AttnPlan& pl, size_t off_ml, size_t off_o, CacheArgs* x) {
+    PartSrc src{};
+    x->block = pl.block;
+    x->blocks = pl.blocks;
+    x->splits = pl.splits;
+    x->ctas = pl.ctas;
+    if (pl.slots == 0) return src;
+    x->part_ml = reinterpret_cast<float2*>(ws + off_ml);
+    x->part_o = reinterpret_cast<float*>(ws + off_o);
+    src.mode = kSplits;
+    src.o = x->part_o;
+    src.ml = x->part_ml;
+    src.block = pl.block;
+    src.blocks = pl.blocks;
+    src.splits = pl.splits;
+    src.ctas = pl.ctas;
+    src.tile = pl.tile;
+    return src;
+  };
+  if (p.has_pre) {
+    CacheArgs x = a;
+    x.k = kp;
+    x.v = vp;
+    x.sk = s.k_prefix;
+    x.sv = s.v_prefix;
+    x.batch = 1;
+    x.n_keys = s.n_prefix;
+    x.rows = s.batch * a.per_seq;
+    x.prefix = 1;
+    x.window = kNoWindow;
+    m.pre = source(p.pre, p.off_pre_ml, p.off_pre_o, &x);
+    CACHE_TRY(launch(p.pre, x));
+  }
+  a.k = k;
+  a.v = v;
+  a.sk = s.k;
+  a.sv = s.v;
+  a.kv_len = kv_len;
+  a.batch = s.batch;
+  a.n_keys = s.n_k;
+  a.rows = a.per_seq;
+  a.window = s.window;
+  a.sinks = s.sinks;
+  m.main = source(p.main, p.off_ml, p.off_o, &a);
+  if (score != nullptr) {
+    a.logits = reinterpret_cast<float*>(ws + p.off_logits);
+    a.pitch = p.pitch;
+    m.final_ml = reinterpret_cast<float2*>(ws + p.off_final);
+  }
+  CACHE_TRY(launch(p.main, a));
+  if (p.main.slots == 0) return CRISP_OK;
+  m.kv_len = kv_len;
+  m.batch = s.batch;
+  m.n_q = s.n_q;
+  m.n_k = s.n_k;
+  m.h_kv = s.h_kv;
+  m.group = s.group;
+  m.window = s.window;
+  m.sinks = s.sinks;
+  m.out = out;
+  m.so = s.out;
+  m.fp32 = s.fp32;
+  CACHE_TRY(launch_cache_merge(m, st));
+  if (score == nullptr) return CRISP_OK;
+  ScoreArgs sc{};
+  sc.logits = a.logits;
+  sc.pitch = p.pitch;
+  sc.final_ml = m.final_ml;
+  sc.kv_len = kv_len;
+  sc.batch = s.batch;
+  sc.n_q = s.n_q;
+  sc.n_k = s.n_k;
+  sc.h_kv = s.h_kv;
+  sc.group = s.group;
+  sc.window = s.window;
+  sc.sinks = s.sinks;
+  sc.score = score;
+  CACHE_TRY(launch_cache_score(sc, st));
+  return CRISP_OK;
+}
+
+// The checks that every operator makes, in the order of the prefill entry points.
+crisp_status prepare_cache(const crisp_cache_cfg* cfg, int op, const void* const* tensors, int n_tensors, CacheShape* s,
+                           CachePlan* p) {
+  crisp_status r = make_cache_shape(cfg, op, s);
+  if (r != CRISP_OK) return r;
+  if ((r = cache_strides(cfg, op, s)) != CRISP_OK) return r;
+  for (int i = 0; i < n_tensors; ++i)
+    if ((r = check_tensor(tensors[i])) != CRISP_OK) return r;
+  *p = plan_cache(*s, op);
+  return check_workspace(cfg, p->total);
+}
+
+}  // namespace
+}  // namespace crisp
+
+using namespace crisp;
+
+extern "C" {
+
+crisp_status crisp_cache_cfg_init(crisp_cache_cfg* cfg, int32_t batch, int32_t n_q, int32_t n_k, int32_t h_q,
+                                  int32_t h_kv, int32_t d, int32_t dtype) {
+  if (cfg == nullptr) return CRISP_ERR_INVALID_ARG;
+  memset(cfg, 0, sizeof(*cfg));
+  cfg->batch = batch;
+  cfg->n_q = n_q;
+  cfg->n_k = n_k;
+  cfg->h_q = h_q;
+  cfg->h_kv = h_kv;
+  cfg->d = d;
+  cfg->dtype = dtype;
+  return CRISP_OK;
+}
+
+crisp_status crisp_cache_workspace_size(const crisp_cache_cfg* cfg, int32_t op, size_t* bytes) {
+  CacheShape s;
+  crisp_status r = make_cache_shape(cfg, op, &s);
+  if (r != CRISP_OK) return r;
+  if (bytes == nullptr) return CRISP_ERR_INVALID_ARG;
+  *bytes = plan_cache(s, op).total;
+  return CRISP_OK;
+}
+
+crisp_status crisp_window_attention(const void* q, const void* k, const void* v, void* out, const int32_t* kv_len,
+                                    const crisp_cache_cfg* cfg, void* stream) {
+  CacheShape s;
+  CachePlan p;
+  const void* t[] = {q, k, v, out};
+  crisp_status r = prepare_cache(cfg, CRISP_CACHE_WINDOW, t, 4, &s, &p);
+  if (r != CRISP_OK) return r;
+  if ((r = check_words(kv_len, true)) != CRISP_OK) return r;
+  return run_attention(q, nullptr, nullptr, k, v, out, nullptr, kv_len, s, p, static_cast<char*>(cfg->workspace),
+                       static_cast<cudaStream_t>(stream));
+}
+
+crisp_status crisp_scored_attention(const void* q, const void* k, const void* v, void* out, float* score,
+                                    const int32_t* kv_len, const crisp_cache_cfg* cfg, void* stream) {
+  CacheShape s;
+  CachePlan p;
+  const void* t[] = {q, k, v, out};
+  crisp_status r = prepare_cache(cfg, CRISP_CACHE_SCORED, t, 4, &s, &p);
+  if (r != CRISP_OK) return r;
+  if ((r = check_words(score, false)) != CRISP_OK) return r;
+  if ((r = check_words(kv_len, true)) != CRISP_OK) return r;
+  return run_attention(q, nullptr, nullptr, k, v, out, score, kv_len, s, p, static_cast<char*>(cfg->workspace),
+                       static_cast<cudaStream_t>(stream));
+}
+
+crisp_status crisp_shared_prefix_attention(const void* q, const void* k_prefix, const void* v_prefix, const void* k,
+                                           const void* v, void* out, const int32_t* kv_len,
+                                           const crisp_cache_cfg* cfg, void* stream) {
+  CacheShape s;
+  CachePlan p;
+  const void* t[] = {q, k_prefix, v_prefix, k, v, out};
+  crisp_status r = prepare_cache(cfg, CRISP_CACHE_PREFIX, t, 6, &s, &p);
+  if (r != CRISP_OK) return r;
+  if ((r = check_words(kv_len, true)) != CRISP_OK) return r;
+  return run_attention(q, k_prefix, v_prefix, k, v, out, nullptr, kv_len, s, p, static_cast<char*>(cfg->workspace),
+                       static_cast<cudaStream_t>(stream));
+}
+
+crisp_status crisp_evict(const void* k, const void* v, const float* score, const int32_t* kv_len, void* k_new,
+                         void* v_new, float* score_new, int32_t* kept, int32_t* new_len,
+                         const crisp_cache_cfg* cfg, void* stream) {
+  CacheShape s;
+  CachePlan p;
+  const void* t[] = {k, v, k_new, v_new};
+  crisp_status r = prepare_cache(cfg, CRISP_CACHE_EVICT, t, 4, &s, &p);
+  if (r != CRISP_OK) return r;
+  const void* words[] = {score, score_new, kept, new_len};
+  for (const void* w : words)
+    if ((r = check_words(w, false)) != CRISP_OK) return r;
+  if ((r = check_words(kv_len, true)) != CRISP_OK) return r;
+  if (kv_len == new_len) return CRISP_ERR_INVALID_ARG;
+  for (int i = 0; i < 2; ++i)
+    for (int j = 2; j < 4; ++j)
+      if (ranges_meet(t[i], i == 0 ? s.k : s.v, s.n_k, t[j], j == 2 ? s.k_new : s.v_new, s.n_new, s))
+        return CRISP_ERR_INVALID_ARG;
+  const int64_t units = (int64_t)s.batch * s.h_kv;
+  if (score < score_new + units * s.n_new && score_new < score + units * s.n_k) return CRISP_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  char* ws = static_cast<char*>(cfg->workspace);
+  CACHE_TRY(cudaMemsetAsync(ws, 0, 32, st));
+  EvictArgs a{};
+  a.k = k;
+  a.v = v;
+  a.score = score;
+  a.kv_len = kv_len;
+  a.k_new = k_new;
+  a.v_new = v_new;
+  a.score_new = score_new;
+  a.kept = kept;
+  a.new_len = new_len;
+  a.status = reinterpret_cast<int32_t*>(ws);
+  a.sk = s.k;
+  a.sv = s.v;
+  a.skn = s.k_new;
+  a.svn = s.v_new;
+  a.batch = s.batch;
+  a.h_kv = s.h_kv;
+  a.n_k = s.n_k;
+  a.sinks = s.sinks;
+  a.recent = s.recent;
+  a.budget = s.budget;
+  a.n_new = s.n_new;
+  a.row_bytes = kHeadDim * (s.fp32 ? 4 : 2);
+  CACHE_TRY(launch_evict(a, st));
+  return CRISP_OK;
+}
+
+crisp_status crisp_cache_device_status(const crisp_cache_cfg* cfg, void* stream, int32_t* device_status) {
+  if (cfg == nullptr || device_status == nullptr) return CRISP_ERR_INVALID_ARG;
+  const crisp_status r = check_workspace(cfg, 256);
+  if (r != CRISP_OK) return r;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int32_t word[8] = {0};
+  CACHE_TRY(cudaStreamSynchronize(st));
+  CACHE_TRY(cudaMemcpy(word, cfg->workspace, sizeof(word), cudaMemcpyDeviceToHost));
+  CACHE_TRY(cudaMemset(cfg->workspace, 0, sizeof(word)));
+  *device_status = word[kStatusCode] != 0 ? word[kStatusCode] : word[kStatusLen];
+  return CRISP_OK;
+}
+
+}  // extern "C"
