@@ -86,8 +86,7 @@ struct PartSrc {
   int block;            // rows per slot
   int blocks;           // row blocks per unit
   int splits;
-  int ctas;
-  int tile;             // kStair: keys per tile
+  const int2* table;    // kStair: [job] first and last CTA
 };
 
 // Arguments shared by the attention kernels.
@@ -100,6 +99,7 @@ struct CacheArgs {
   int n_keys;              // key slots per sequence, or the prefix length
   int h_kv, group, n_q, window, sinks;
   int rows, per_seq;       // rows per unit; rows per sequence within it
+  int sets_status;         // the call's only kernel that reports: it sets the status words instead of a memset
   int prefix;              // rows run over every sequence, every key is seen
   float scale_log2;
   Strides sq, sk, sv, so;
@@ -107,6 +107,7 @@ struct CacheArgs {
   float* part_o;
   float2* part_ml;
   int block, blocks, splits, ctas;
+  int2* table;             // decode kernel: [job] first and last CTA that had a tile of it
   // scored: scaled logits [unit][row][pitch] by list index
   float* logits;
   int64_t pitch;
@@ -158,6 +159,75 @@ __device__ __forceinline__ int row_pos(const CacheArgs& a, int len, int i) {
   return a.prefix ? (1 << 29) : len - a.n_q + i;
 }
 
+__device__ __forceinline__ int clamp_len(const int32_t* kv_len, int b, int n_keys, bool* bad = nullptr) {
+  if (kv_len == nullptr) return n_keys;
+  const int n = kv_len[b];
+  if (n >= 0 && n <= n_keys) return n;
+  if (bad != nullptr) *bad = true;
+  return n < 0 ? 0 : n_keys;
+}
+__device__ __forceinline__ int clamped_len(const CacheArgs& a, int b) { return clamp_len(a.kv_len, b, a.n_keys); }
+
+// Key tiles of every sequence, summed: cum[b] = tiles of the sequences before
+// b, cum[batch] = all. Called by a whole CTA; ends with a barrier. tmp: int[32].
+// Returns whether some length was outside [0, n_keys].
+__device__ __forceinline__ bool stair_scan(const int32_t* kv_len, int batch, int n_keys, int n_q, int window, int sinks,
+                                           bool prefix, int tile, int* cum, int* tmp) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (batch + blockDim.x - 1) / blockDim.x;
+  bool bad = false;
+  auto tiles_of = [&](int b) {
+    const int n = clamp_len(kv_len, b, n_keys, &bad);
+    return ((prefix ? n : key_list(n, n_q, 0, n_q - 1, window, sinks).total) + tile - 1) / tile;
+  };
+  if (batch == 1) {
+    if (tid == 0) {
+      cum[0] = 0;
+      cum[1] = tiles_of(0);
+    }
+    return __syncthreads_or(bad) != 0;
+  }
+  int mine = 0;
+  for (int i = 0; i < per; ++i) {
+    const int b = tid * per + i;
+    if (b < batch) mine += tiles_of(b);
+  }
+  int inc = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, inc, d);
+    if (lane >= d) inc += y;
+  }
+  if (lane == 31) tmp[warp] = inc;
+  __syncthreads();
+  int at = inc - mine;
+  for (int w = 0; w < warp; ++w) at += tmp[w];
+  for (int i = 0; i < per; ++i) {
+    const int b = tid * per + i;
+    if (b < batch) {
+      cum[b] = at;
+      at += tiles_of(b);
+      if (b == batch - 1) cum[batch] = at;
+    }
+  }
+  return __syncthreads_or(bad) != 0;
+}
+
+// Programmatic launch: let the next kernel of the stream start its set-up
+// early / wait until the kernels before have finished and their writes show.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_launches() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// The sequence that holds tile x of the summed list (sequences without tiles are passed over).
+__device__ __forceinline__ int stair_find(const int* cum, int batch, int x) {
+  int lo = 0, hi = batch - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (cum[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
 }  // namespace dev
 #endif
 
@@ -174,36 +244,32 @@ struct CachePlan {
   AttnPlan main, pre;       // the sequences' own keys; the shared prefix
   bool has_pre;
   int64_t pitch;            // scored: logits per row
-  size_t off_ml, off_o, off_pre_ml, off_pre_o, off_logits, off_final;
-  size_t off_thresh;        // evict
+  int warps_per_row;        // of the finishing kernel
+  size_t off_ml, off_o, off_table, off_pre_ml, off_pre_o, off_pre_table, off_logits;
   size_t total;
 };
 
 CachePlan plan_cache(const CacheShape& s, int op);
 
 // ---- launchers (each enqueues on `st`; return cudaGetLastError()) ----
+cudaError_t launch_cache_decode(const CacheArgs& a, const AttnPlan& p, cudaStream_t st);
 cudaError_t launch_cache_tile(const CacheArgs& a, const AttnPlan& p, bool fp32, cudaStream_t st);
 
-struct MergeArgs {
+struct FinishArgs {
   PartSrc main, pre;
   const int32_t* kv_len;
-  int batch, n_q, n_k, h_kv, group, window, sinks;
+  int batch, n_q, n_k, n_prefix, h_kv, group, window, sinks;
   void* out;
   Strides so;
   bool fp32;
-  float2* final_ml;   // scored: [unit][row] (maximum, 1 / sum); NULL otherwise
-};
-cudaError_t launch_cache_merge(const MergeArgs& a, cudaStream_t st);
-
-struct ScoreArgs {
-  const float* logits;
+  int warps_per_row;       // 1, 2, 4 or 8
+  // scored
+  const float* logits;     // [unit][row][pitch], by list index; NULL: no scores
   int64_t pitch;
-  const float2* final_ml;
-  const int32_t* kv_len;
-  int batch, n_q, n_k, h_kv, group, window, sinks;
-  float* score;       // [batch][h_kv][n_k]
+  float* score;            // [batch][h_kv][n_k]
+  int out_ctas, score_ctas;   // set by the launcher; score CTAs per unit
 };
-cudaError_t launch_cache_score(const ScoreArgs& a, cudaStream_t st);
+cudaError_t launch_cache_finish(const FinishArgs& a, cudaStream_t st);
 
 struct EvictArgs {
   const void *k, *v;

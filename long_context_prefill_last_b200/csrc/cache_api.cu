@@ -137,6 +137,21 @@ AttnPlan plan_tile(int units, int rows, int keys) {
   return p;
 }
 
+// Grid of the bf16 decode kernel: two CTAs per SM, or one per key tile when
+// there are fewer.
+AttnPlan plan_decode(int units, int rows, int keys) {
+  AttnPlan p{};
+  p.kernel = kDecodeMma;
+  p.units = units;
+  p.tile = 64;
+  p.block = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  p.blocks = (rows + p.block - 1) / p.block;
+  const int64_t jobs = (int64_t)units * p.blocks;
+  p.ctas = (int)std::min<int64_t>(2 * kSms, jobs * ((keys + 63) / 64));
+  p.slots = (size_t)(jobs + p.ctas);
+  return p;
+}
+
 }  // namespace
 
 CachePlan plan_cache(const CacheShape& s, int op) {
@@ -147,7 +162,8 @@ CachePlan plan_cache(const CacheShape& s, int op) {
     off = align256(off + bytes);
     return o;
   };
-  auto parts = [&](AttnPlan& a, size_t* ml, size_t* o) {
+  auto parts = [&](AttnPlan& a, size_t* ml, size_t* o, size_t* table) {
+    *table = take(a.kernel == kDecodeMma ? (size_t)a.units * a.blocks * 8 : 0);
     *ml = take(a.slots * a.block * 8);
     *o = take(a.slots * a.block * kHeadDim * 4);
   };
@@ -156,15 +172,26 @@ CachePlan plan_cache(const CacheShape& s, int op) {
     const int64_t seen = (int64_t)s.window + s.sinks + s.n_q - 1;
     const int keys = (int)std::min<int64_t>(s.n_k, seen);
     p.has_pre = op == CRISP_CACHE_PREFIX;
-    p.main = plan_tile(units, rows, keys);
-    if (p.has_pre) p.pre = plan_tile(s.h_kv, s.batch * rows, s.n_prefix);
-    if (op == CRISP_CACHE_WINDOW && p.main.splits == 1) p.main.slots = 0;   // output rows straight away
-    parts(p.main, &p.off_ml, &p.off_o);
-    if (p.has_pre) parts(p.pre, &p.off_pre_ml, &p.off_pre_o);
+    // bf16 drafts take the decode kernel, as does a prefix read by at most 64 rows
+    const bool draft = !s.fp32 && s.n_q <= kMaxDraft;
+    p.main = draft ? plan_decode(units, rows, keys) : plan_tile(units, rows, keys);
+    if (p.has_pre) {
+      const int all = s.batch * rows;
+      p.pre = !s.fp32 && all <= 64 ? plan_decode(s.h_kv, all, s.n_prefix) : plan_tile(s.h_kv, all, s.n_prefix);
+    }
+    // output rows straight away when no row's keys are split
+    if (op == CRISP_CACHE_WINDOW && p.main.kernel != kDecodeMma && p.main.splits == 1) p.main.slots = 0;
+    // a row's pieces are read by one warp while there are few, by up to eight when there are many
+    auto pieces = [](const AttnPlan& a) {
+      return a.slots == 0 ? 0 : a.kernel == kDecodeMma ? a.ctas / (a.units * a.blocks) + 1 : a.splits;
+    };
+    const int most = pieces(p.main) + pieces(p.pre);
+    p.warps_per_row = most > 16 ? 8 : most > 8 ? 4 : most > 4 ? 2 : 1;
+    parts(p.main, &p.off_ml, &p.off_o, &p.off_table);
+    if (p.has_pre) parts(p.pre, &p.off_pre_ml, &p.off_pre_o, &p.off_pre_table);
     if (op == CRISP_CACHE_SCORED) {
       p.pitch = (keys + 63) / 64 * 64;
       p.off_logits = take((size_t)units * rows * p.pitch * 4);
-      p.off_final = take((size_t)units * rows * 8);
     }
   }
   p.total = off;
@@ -185,8 +212,12 @@ crisp_status run_attention(const void* q, const void* kp, const void* vp, const 
                            float* score, const int32_t* kv_len, const CacheShape& s, const CachePlan& p, char* ws,
                            cudaStream_t st) {
   int32_t* status = reinterpret_cast<int32_t*>(ws);
-  CACHE_TRY(cudaMemsetAsync(status, 0, 32, st));
-  auto launch = [&](const AttnPlan& pl, const CacheArgs& a) { return launch_cache_tile(a, pl, s.fp32, st); };
+  // a decode kernel on its own sets the status words; otherwise they are cleared first and kernels only report
+  const bool clear = p.main.kernel != kDecodeMma || (p.has_pre && p.pre.kernel != kDecodeMma);
+  if (clear) CACHE_TRY(cudaMemsetAsync(status, 0, 32, st));
+  auto launch = [&](const AttnPlan& pl, const CacheArgs& a) {
+    return pl.kernel == kDecodeMma ? launch_cache_decode(a, pl, st) : launch_cache_tile(a, pl, s.fp32, st);
+  };
   CacheArgs a{};
   a.q = q;
   a.out = out;
@@ -198,8 +229,8 @@ crisp_status run_attention(const void* q, const void* kp, const void* vp, const 
   a.scale_log2 = s.scale_log2;
   a.sq = s.q;
   a.so = s.out;
-  MergeArgs m{};
-  auto source = [&](const AttnPlan& pl, size_t off_ml, size_t off_o, CacheArgs* x) {
+  FinishArgs m{};
+  auto source = [&](const AttnPlan& pl, size_t off_ml, size_t off_o, size_t off_table, CacheArgs* x) {
     PartSrc src{};
     x->block = pl.block;
     x->blocks = pl.blocks;
@@ -208,14 +239,13 @@ crisp_status run_attention(const void* q, const void* kp, const void* vp, const 
     if (pl.slots == 0) return src;
     x->part_ml = reinterpret_cast<float2*>(ws + off_ml);
     x->part_o = reinterpret_cast<float*>(ws + off_o);
-    src.mode = kSplits;
+    src.mode = pl.kernel == kDecodeMma ? kStair : kSplits;
     src.o = x->part_o;
     src.ml = x->part_ml;
     src.block = pl.block;
     src.blocks = pl.blocks;
     src.splits = pl.splits;
-    src.ctas = pl.ctas;
-    src.tile = pl.tile;
+    src.table = x->table = reinterpret_cast<int2*>(ws + off_table);
     return src;
   };
   if (p.has_pre) {
@@ -229,7 +259,7 @@ crisp_status run_attention(const void* q, const void* kp, const void* vp, const 
     x.rows = s.batch * a.per_seq;
     x.prefix = 1;
     x.window = kNoWindow;
-    m.pre = source(p.pre, p.off_pre_ml, p.off_pre_o, &x);
+    m.pre = source(p.pre, p.off_pre_ml, p.off_pre_o, p.off_pre_table, &x);
     CACHE_TRY(launch(p.pre, x));
   }
   a.k = k;
@@ -242,11 +272,14 @@ crisp_status run_attention(const void* q, const void* kp, const void* vp, const 
   a.rows = a.per_seq;
   a.window = s.window;
   a.sinks = s.sinks;
-  m.main = source(p.main, p.off_ml, p.off_o, &a);
+  a.sets_status = clear ? 0 : 1;
+  m.main = source(p.main, p.off_ml, p.off_o, p.off_table, &a);
   if (score != nullptr) {
     a.logits = reinterpret_cast<float*>(ws + p.off_logits);
     a.pitch = p.pitch;
-    m.final_ml = reinterpret_cast<float2*>(ws + p.off_final);
+    m.logits = a.logits;
+    m.pitch = p.pitch;
+    m.score = score;
   }
   CACHE_TRY(launch(p.main, a));
   if (p.main.slots == 0) return CRISP_OK;
@@ -254,6 +287,7 @@ crisp_status run_attention(const void* q, const void* kp, const void* vp, const 
   m.batch = s.batch;
   m.n_q = s.n_q;
   m.n_k = s.n_k;
+  m.n_prefix = s.n_prefix;
   m.h_kv = s.h_kv;
   m.group = s.group;
   m.window = s.window;
@@ -261,22 +295,8 @@ crisp_status run_attention(const void* q, const void* kp, const void* vp, const 
   m.out = out;
   m.so = s.out;
   m.fp32 = s.fp32;
-  CACHE_TRY(launch_cache_merge(m, st));
-  if (score == nullptr) return CRISP_OK;
-  ScoreArgs sc{};
-  sc.logits = a.logits;
-  sc.pitch = p.pitch;
-  sc.final_ml = m.final_ml;
-  sc.kv_len = kv_len;
-  sc.batch = s.batch;
-  sc.n_q = s.n_q;
-  sc.n_k = s.n_k;
-  sc.h_kv = s.h_kv;
-  sc.group = s.group;
-  sc.window = s.window;
-  sc.sinks = s.sinks;
-  sc.score = score;
-  CACHE_TRY(launch_cache_score(sc, st));
+  m.warps_per_row = p.warps_per_row;
+  CACHE_TRY(launch_cache_finish(m, st));
   return CRISP_OK;
 }
 

@@ -1,0 +1,402 @@
+// Decode attention over a key/value cache, bf16: a few query rows per
+// key/value head (tokens of a draft x query heads of the group, up to 64)
+// against a long key list, in one pass with running softmax statistics.
+//
+// Bound: HBM. A key costs 512 bytes per key/value head and 4 * 128 FLOP per
+// row, so at 64 rows the legacy tensor instruction (m16n8k16, operands in
+// registers) still keeps up with memory, and with 4 .. 28 rows a tcgen05 tile
+// of 128 rows would compute mostly padding. Keys and values come through a
+// three-stage cp.async ring (64 keys x 512 bytes a stage, two CTAs per SM);
+// per-row copies let the key list jump from the first keys to the window
+// without a hole, and zero-fill past its end.
+//
+// The key tiles of all jobs (sequence, key/value head, row block) form one
+// list that is dealt to the CTAs in equal runs, so a ragged batch keeps every
+// SM busy however its lengths lie; the lengths are read on the device, and the
+// ring runs on across jobs. Each (CTA, job) pair leaves one partial result,
+// joined by cache_merge.cu.
+//
+// 4 warps: RT = 1, 2 or 4 of them along the rows (16 each), 4 / RT along the
+// keys of a tile; warps that share rows are joined in shared memory at the
+// end of a job's run.
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include "cache.h"
+#include "ptx.cuh"
+
+namespace crisp {
+namespace {
+
+constexpr int kKeys = 64;
+constexpr int kStages = 3;
+constexpr int kThreads = 128;
+constexpr uint32_t kTileBytes = kKeys * kHeadDim * 2;   // K or V of one stage
+constexpr uint32_t kStageBytes = 2 * kTileBytes;
+constexpr int kOPitch = 64 + 4;                          // floats per row of the join buffer (half the columns)
+constexpr uint32_t OFF_JOIN = kStages * kStageBytes;     // 2 x 16 rows
+constexpr uint32_t OFF_ML = OFF_JOIN + 2 * 16 * kOPitch * 4;
+constexpr uint32_t OFF_CUM = OFF_ML + 4 * 16 * 8;        // int[batch + 1]
+constexpr uint32_t smem_bytes(int batch) { return OFF_CUM + 4 * (batch + 1); }
+static_assert(2 * (smem_bytes(kMaxBatch) + 1024 + 128) <= 228 * 1024, "two CTAs per SM");
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int RT>
+__global__ void __launch_bounds__(kThreads, 2) cache_decode_kernel(CacheArgs a) {
+  constexpr int KW = 4 / RT;            // warps along the keys
+  constexpr int NK = kKeys / KW;        // keys of a tile per warp
+  constexpr int NT = NK / 8;            // 8-key accumulator tiles per warp
+  constexpr int BLOCK = 16 * RT;        // rows per job
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int scan_tmp[32];
+  int* cum = reinterpret_cast<int*>(smem + OFF_CUM);
+  const uint32_t sbase = dev::smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rt = warp % RT, kw = warp / RT;
+  const int gq = lane >> 2, tq = lane & 3;
+
+  dev::launch_dependents();
+  const bool bad = dev::stair_scan(a.kv_len, a.batch, a.n_keys, a.n_q, a.window, a.sinks, a.prefix != 0, kKeys, cum,
+                                   scan_tmp);
+  if (blockIdx.x == 0 && tid == 0) {
+    if (a.sets_status) a.status[kStatusCode] = 0;
+    if (a.sets_status || bad) a.status[kStatusLen] = bad ? CRISP_ERR_INVALID_ARG : 0;
+  }
+  const int per_seq = a.h_kv * a.blocks;                       // jobs per sequence
+  const int64_t all = (int64_t)cum[a.batch] * per_seq;
+  const int64_t ctas = all < a.ctas ? all : a.ctas;            // every one of them has a tile
+  if (blockIdx.x >= ctas) return;
+  const int64_t x0 = all * blockIdx.x / ctas;
+  const int n_all = (int)(all * (blockIdx.x + 1) / ctas - x0);
+
+  // a place in the flat tile list
+  struct Place {
+    int b, jj, t, T, len;
+    KeyList list;
+  };
+  auto enter = [&](Place& p) {   // after b, jj, t are set
+    p.T = cum[p.b + 1] - cum[p.b];
+    p.len = dev::clamped_len(a, p.b);
+    p.list = dev::unit_keys(a, p.len, 0, a.n_q - 1);
+  };
+  auto next_job = [&](Place& p) {
+    p.t = 0;
+    if (++p.jj == per_seq) {
+      p.jj = 0;
+      do ++p.b; while (cum[p.b + 1] == cum[p.b]);
+      enter(p);
+    }
+  };
+  Place ld;
+  ld.b = dev::stair_find(cum, a.batch, (int)(x0 / per_seq));
+  {
+    const int64_t rem = x0 - (int64_t)cum[ld.b] * per_seq;
+    const int T = cum[ld.b + 1] - cum[ld.b];
+    ld.jj = (int)(rem / T);
+    ld.t = (int)(rem - (int64_t)ld.jj * T);
+  }
+  enter(ld);
+  Place cp = ld;
+
+  // The loads run kStages - 1 tiles ahead of the arithmetic, across jobs.
+  const int lrow = tid >> 4, lchunk = tid & 15;
+  const char *kp, *vp;
+  auto bind = [&]() {
+    const int g = ld.jj / a.blocks;
+    kp = static_cast<const char*>(a.k) + (ld.b * a.sk.seq + g * a.sk.head) * 2 + lchunk * 16;
+    vp = static_cast<const char*>(a.v) + (ld.b * a.sv.seq + g * a.sv.head) * 2 + lchunk * 16;
+  };
+  bind();
+  int loaded = 0;
+  auto load = [&]() {
+    if (loaded < n_all) {
+      if (ld.t == ld.T) {
+        next_job(ld);
+        bind();
+      }
+      const uint32_t dst = sbase + (loaded % kStages) * kStageBytes + lrow * 256 + ((lchunk ^ lrow) << 4);
+#pragma unroll
+      for (int i = 0; i < kKeys / 8; ++i) {
+        const int u = ld.t * kKeys + i * 8 + lrow;
+        const bool in = u < ld.list.total;
+        const int64_t j = in ? ld.list.key(u) : 0;
+        cp16(dst + i * 8 * 256, kp + j * a.sk.token * 2, in ? 16u : 0u);
+        cp16(dst + kTileBytes + i * 8 * 256, vp + j * a.sv.token * 2, in ? 16u : 0u);
+      }
+      ++ld.t;
+      ++loaded;
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) load();
+
+  int done = 0;
+  while (done < n_all) {
+    const int run = n_all - done < cp.T - cp.t ? n_all - done : cp.T - cp.t;   // tiles of this job here
+    const int g = cp.jj / a.blocks, rb = cp.jj - g * a.blocks;
+    const int unit = cp.b * a.h_kv + g;
+    const int r0 = rb * BLOCK + rt * 16;                        // this warp's first row
+    const KeyList list = cp.list;
+
+    // Q fragments (rows past the unit's end are zero) and the rows' positions
+    uint32_t qf[8][4];
+    int pos[2];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int r = r0 + half * 8 + gq;
+      const bool in = r < a.rows;
+      const dev::Row w = dev::unit_row(a, cp.b, g, in ? r : 0);
+      const uint32_t* qp = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.q) + w.b * a.sq.seq +
+                                                             w.h * a.sq.head + w.i * a.sq.token) + tq;
+      pos[half] = in ? dev::row_pos(a, cp.len, w.i) : -1;
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) {
+        qf[ks][half] = in ? qp[ks * 8] : 0u;
+        qf[ks][2 + half] = in ? qp[ks * 8 + 4] : 0u;
+      }
+    }
+    float o[16][4];
+#pragma unroll
+    for (int n = 0; n < 16; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, lc[2] = {0.f, 0.f};
+    const int first_pos = a.prefix ? (1 << 29) : cp.len - a.n_q, last_pos = a.prefix ? 0 : cp.len - 1;
+
+    for (int it = 0; it < run; ++it) {
+      cp_wait<kStages - 2>();
+      __syncthreads();
+      load();
+      const int t = cp.t + it;
+      const uint32_t ks_base = sbase + ((done + it) % kStages) * kStageBytes, vs_base = ks_base + kTileBytes;
+      float s[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+        for (int n2 = 0; n2 < NT / 2; ++n2) {
+          const int key = kw * NK + n2 * 16 + ((lane >> 4) << 3) + (lane & 7);
+          const int chunk = ks * 2 + ((lane >> 3) & 1);
+          uint32_t f[4];
+          ldsm4(ks_base + key * 256 + ((chunk ^ (key & 7)) << 4), f);
+          mma16816(s[2 * n2], qf[ks], f[0], f[1]);
+          mma16816(s[2 * n2 + 1], qf[ks], f[2], f[3]);
+        }
+      // scaled logits; unseen keys get -inf. Tiles whose every key every row sees skip the tests.
+      const int u_last = t * kKeys + kKeys - 1;
+      const int wu = t * kKeys > list.se ? t * kKeys : list.se;    // first entry of the window's part
+      const bool whole = u_last < list.total && list.key(u_last) <= first_pos &&
+                         (u_last < list.se || list.key(wu) > last_pos - a.window);
+      float tmax[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float y = s[n][e] * a.scale_log2;
+          if (!whole) {
+            const int u = t * kKeys + kw * NK + n * 8 + tq * 2 + (e & 1), key = list.key(u), p = pos[e >> 1];
+            const bool seen = u < list.total && key <= p && (key < a.sinks || key > p - a.window);
+            y = seen ? y : -INFINITY;
+          }
+          s[n][e] = y;
+          tmax[e >> 1] = fmaxf(tmax[e >> 1], y);
+        }
+      if (a.logits != nullptr) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int r = r0 + half * 8 + gq;
+          if (r < a.rows) {
+            float* dst = a.logits + ((int64_t)unit * a.rows + r) * a.pitch + t * kKeys + kw * NK + tq * 2;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              *reinterpret_cast<float2*>(dst + n * 8) = make_float2(s[n][2 * half], s[n][2 * half + 1]);
+          }
+        }
+      }
+      float base[2], f[2];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        tmax[half] = fmaxf(tmax[half], __shfl_xor_sync(0xffffffffu, tmax[half], 1));
+        tmax[half] = fmaxf(tmax[half], __shfl_xor_sync(0xffffffffu, tmax[half], 2));
+        const float mn = fmaxf(m[half], tmax[half]);
+        base[half] = mn == -INFINITY ? 0.f : mn;
+        f[half] = dev::ex2(m[half] - base[half]);
+        m[half] = mn;
+      }
+      if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+        l[0] *= f[0], lc[0] *= f[0];
+        l[1] *= f[1], lc[1] *= f[1];
+#pragma unroll
+        for (int n = 0; n < 16; ++n) {
+          o[n][0] *= f[0];
+          o[n][1] *= f[0];
+          o[n][2] *= f[1];
+          o[n][3] *= f[1];
+        }
+      }
+      float part[2] = {0.f, 0.f};
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[n][e] = dev::ex2(s[n][e] - base[e >> 1]);
+          part[e >> 1] += s[n][e];
+        }
+      // the running sum is compensated (Kahan): scores need it to a few 2^-24
+      // after thousands of tiles
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const float y = part[half] - lc[half], z = l[half] + y;
+        lc[half] = (z - l[half]) - y;
+        l[half] = z;
+      }
+      // weights rounded to bf16 for the product with V (fp32 accumulation); l keeps them in fp32
+#pragma unroll
+      for (int k16 = 0; k16 < NT / 2; ++k16) {
+        const uint32_t pf[4] = {dev::pack_bf16x2(s[2 * k16][0], s[2 * k16][1]),
+                                dev::pack_bf16x2(s[2 * k16][2], s[2 * k16][3]),
+                                dev::pack_bf16x2(s[2 * k16 + 1][0], s[2 * k16 + 1][1]),
+                                dev::pack_bf16x2(s[2 * k16 + 1][2], s[2 * k16 + 1][3])};
+        const int key = kw * NK + k16 * 16 + (lane & 15);
+#pragma unroll
+        for (int d2 = 0; d2 < 8; ++d2) {
+          const int chunk = d2 * 2 + (lane >> 4);
+          uint32_t vf[4];
+          ldsm4_t(vs_base + key * 256 + ((chunk ^ (key & 7)) << 4), vf);
+          mma16816(o[2 * d2], pf, vf[0], vf[1]);
+          mma16816(o[2 * d2 + 1], pf, vf[2], vf[3]);
+        }
+      }
+    }
+
+    // join the warps that share rows: common maximum, then a tree over the
+    // warps, half the columns at a time
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
+      l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
+    }
+    if constexpr (KW > 1) {
+      float* buf = reinterpret_cast<float*>(smem + OFF_JOIN);
+      float2* sml = reinterpret_cast<float2*>(smem + OFF_ML);
+      if (tq == 0) {
+        sml[warp * 16 + gq] = make_float2(m[0], l[0]);
+        sml[warp * 16 + 8 + gq] = make_float2(m[1], l[1]);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int c = 0; c < KW; ++c) M = fmaxf(M, sml[(rt + RT * c) * 16 + half * 8 + gq].x);
+        const float bs = M == -INFINITY ? 0.f : M;
+#pragma unroll
+        for (int c = 0; c < KW; ++c) {
+          const float2 ml = sml[(rt + RT * c) * 16 + half * 8 + gq];
+          L += dev::ex2(ml.x - bs) * ml.y;
+        }
+        const float w = dev::ex2(m[half] - bs);
+        m[half] = M;
+        l[half] = L;
+#pragma unroll
+        for (int n = 0; n < 16; ++n) {
+          o[n][2 * half] *= w;
+          o[n][2 * half + 1] *= w;
+        }
+      }
+#pragma unroll
+      for (int far = KW / 2; far >= 1; far >>= 1)   // warps far .. 2 far - 1 hand over to 0 .. far - 1
+#pragma unroll
+        for (int c0 = 0; c0 < 16; c0 += 8) {
+          if (kw >= far && kw < 2 * far) {
+            float* dst = buf + (((kw - far) * RT + rt) * 16 + gq) * kOPitch + tq * 2;
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+              *reinterpret_cast<float2*>(dst + n * 8) = make_float2(o[c0 + n][0], o[c0 + n][1]);
+              *reinterpret_cast<float2*>(dst + 8 * kOPitch + n * 8) = make_float2(o[c0 + n][2], o[c0 + n][3]);
+            }
+          }
+          __syncthreads();
+          if (kw < far) {
+            const float* src = buf + ((kw * RT + rt) * 16 + gq) * kOPitch + tq * 2;
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+              const float2 u = *reinterpret_cast<const float2*>(src + n * 8);
+              const float2 v = *reinterpret_cast<const float2*>(src + 8 * kOPitch + n * 8);
+              o[c0 + n][0] += u.x, o[c0 + n][1] += u.y;
+              o[c0 + n][2] += v.x, o[c0 + n][3] += v.y;
+            }
+          }
+          __syncthreads();
+        }
+    }
+    if (kw == 0) {
+      const int64_t slot = (int64_t)blockIdx.x + (int64_t)cp.b * per_seq + cp.jj;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (r0 + half * 8 + gq >= a.rows) continue;
+        const int64_t at = slot * BLOCK + rt * 16 + half * 8 + gq;
+        float* dst = a.part_o + at * kHeadDim + tq * 2;
+#pragma unroll
+        for (int n = 0; n < 16; ++n)
+          *reinterpret_cast<float2*>(dst + n * 8) = make_float2(o[n][2 * half], o[n][2 * half + 1]);
+        if (tq == 0) a.part_ml[at] = make_float2(m[half], l[half]);
+      }
+    }
+    if (tid == 0) {
+      int* entry = reinterpret_cast<int*>(a.table + cp.b * per_seq + cp.jj);
+      if (cp.t == 0) entry[0] = blockIdx.x;
+      if (cp.t + run == cp.T) entry[1] = blockIdx.x;
+    }
+    done += run;
+    cp.t += run;
+    if (cp.t == cp.T && done < n_all) next_job(cp);
+  }
+}
+
+template <int RT>
+cudaError_t launch(const CacheArgs& a, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(cache_decode_kernel<RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       smem_bytes(kMaxBatch));
+  if (e != cudaSuccess) return e;
+  cache_decode_kernel<RT><<<a.ctas, kThreads, smem_bytes(a.batch), st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_decode(const CacheArgs& a, const AttnPlan& p, cudaStream_t st) {
+  if (p.block == 16) return launch<1>(a, st);
+  if (p.block == 32) return launch<2>(a, st);
+  return launch<4>(a, st);
+}
+
+}  // namespace crisp

@@ -1,8 +1,12 @@
 // Joins the partial results of split key lists, and adds softmax weights to
 // the keys' accumulated scores.
 //   M = max_i m_i, L = sum_i 2^(m_i - M) l_i, o = sum_i 2^(m_i - M) O_i / L
-// The pieces of a row are joined in slot order, so the result does not depend
-// on the order in which CTAs ran.
+//   score_j += sum over the rows of 2^(x_rj - M_r) / L_r
+// The pieces of a row are joined in a fixed order and a thread adds up a key's
+// rows in order, so results do not depend on the order in which CTAs ran.
+// Bound by latency (a few KB per row), so both happen in one launch: the first
+// CTAs take output rows, the others keys, each of them computing the (M, L)
+// that it needs from the pieces' own.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -12,87 +16,222 @@
 namespace crisp {
 namespace {
 
-__device__ __forceinline__ int merge_len(const int32_t* kv_len, int b, int n) {
-  if (kv_len == nullptr) return n;
-  const int x = kv_len[b];
-  return x < 0 ? 0 : (x > n ? n : x);
-}
+constexpr int kThreads = 256;
+constexpr int kScoreKeys = 4;   // keys per thread, a CTA's width apart
+constexpr int kScoreRows = 4;   // rows per step
 
-// One CTA per output row (sequence, query head, token); thread = column.
-template <typename T>
-__global__ void __launch_bounds__(128) cache_merge_kernel(MergeArgs a) {
-  const int row = blockIdx.x, c = threadIdx.x;
-  const int i = row % a.n_q, bh = row / a.n_q;
-  const int h_q = a.h_kv * a.group;
-  const int b = bh / h_q, h = bh - b * h_q;
-  const int g = h / a.group, j = h - g * a.group;
-  float M = -INFINITY, L = 0.f, o = 0.f;
+struct Pieces {
+  int64_t at[2];   // first piece's row, in rows of the source
+  int count[2];
+};
+
+// The pieces of row r of unit (b, g) in both sources.
+__device__ __forceinline__ Pieces find_pieces(const FinishArgs& a, int b, int g, int i, int j) {
+  Pieces p;
+#pragma unroll
   for (int src = 0; src < 2; ++src) {
-    const PartSrc& p = src == 0 ? a.main : a.pre;
-    if (p.mode == kPartNone) continue;
+    const PartSrc& s = src == 0 ? a.main : a.pre;
+    p.count[src] = 0;
+    p.at[src] = 0;
+    if (s.mode == kPartNone) continue;
     const int unit = src == 0 ? b * a.h_kv + g : g;
     const int r = src == 0 ? i * a.group + j : (b * a.n_q + i) * a.group + j;
-    const int blk = r / p.block, in = r - blk * p.block;
-    const int64_t first = ((int64_t)unit * p.blocks + blk) * p.splits;
-    const int count = p.splits;
-    for (int s = 0; s < count; ++s) {
-      const int64_t at = (first + s) * p.block + in;
-      const float2 ml = p.ml[at];
-      if (ml.y == 0.f) continue;   // the piece holds no key that this row sees
-      const float x = p.o[at * kHeadDim + c];
-      const float mn = fmaxf(M, ml.x);
-      const float f0 = exp2f(M - mn), f1 = exp2f(ml.x - mn);
-      L = L * f0 + ml.y * f1;
-      o = o * f0 + x * f1;
-      M = mn;
+    const int blk = r / s.block, in = r - blk * s.block;
+    const int job = unit * s.blocks + blk;
+    int64_t first = (int64_t)job * s.splits;
+    int count = s.splits;
+    if (s.mode == kStair) {
+      // a job without key tiles has no entry of its own
+      const bool any = src == 1 || dev::clamp_len(a.kv_len, b, a.n_k) > 0;
+      const int2 ctas = any ? s.table[job] : make_int2(0, -1);
+      first = (int64_t)ctas.x + job;
+      count = ctas.y - ctas.x + 1;
     }
+    p.at[src] = first * s.block + in;
+    p.count[src] = count;
   }
-  const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);   // no key: 0; NaN stays NaN
-  T* dst = static_cast<T*>(a.out) + b * a.so.seq + h * a.so.head + i * a.so.token;
-  dst[c] = dev::from_f32<T>(o * inv);
-  if (a.final_ml != nullptr && c == 0)
-    a.final_ml[(int64_t)(b * a.h_kv + g) * a.n_q * a.group + i * a.group + j] = make_float2(M == -INFINITY ? 0.f : M, inv);
+  return p;
 }
 
-// score[key] += sum over the unit's rows of 2^(x - M) / L, a thread per key
-// and the rows in order: no atomics, the sum's order is fixed.
-__global__ void __launch_bounds__(256) cache_score_kernel(ScoreArgs a) {
-  extern __shared__ float2 fin[];
-  const int unit = blockIdx.y, b = unit / a.h_kv;
-  const int rows = a.n_q * a.group;
-  for (int r = threadIdx.x; r < rows; r += blockDim.x) fin[r] = a.final_ml[(int64_t)unit * rows + r];
-  __syncthreads();
-  const KeyList list = key_list(merge_len(a.kv_len, b, a.n_k), a.n_q, 0, a.n_q - 1, a.window, a.sinks);
-  const int u = blockIdx.x * blockDim.x + threadIdx.x;
-  if (u >= list.total) return;
-  const float* x = a.logits + (int64_t)unit * rows * a.pitch + u;
-  float sum = 0.f;
-  for (int r = 0; r < rows; ++r) {
-    const float y = x[r * a.pitch];
-    if (y != -INFINITY) sum += exp2f(y - fin[r].x) * fin[r].y;   // -inf: the row does not see the key
+__device__ __forceinline__ float2 piece_ml(const FinishArgs& a, const Pieces& p, int i) {
+  const bool own = i < p.count[0];
+  const PartSrc& s = own ? a.main : a.pre;
+  return s.ml[p.at[own ? 0 : 1] + (int64_t)(own ? i : i - p.count[0]) * s.block];
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+  return x;
+}
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+  return x;
+}
+
+// Row statistics by one warp: the base that exponents subtract (0 when the row
+// sees no key) and the sum.
+__device__ __forceinline__ float2 row_stats(const FinishArgs& a, const Pieces& p, int lane) {
+  const int n = p.count[0] + p.count[1];
+  float M = -INFINITY;
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, piece_ml(a, p, i).x);
+  M = warp_max(M);
+  const float base = M == -INFINITY ? 0.f : M;
+  float L = 0.f;
+  for (int i = lane; i < n; i += 32) {
+    const float2 ml = piece_ml(a, p, i);
+    L += exp2f(ml.x - base) * ml.y;
   }
-  float* dst = a.score + (int64_t)unit * a.n_k + list.key(u);
-  *dst += sum;
+  return make_float2(base, warp_sum(L));
+}
+
+// 1 / L; 0 for a row that sees no key; NaN stays NaN.
+__device__ __forceinline__ float inverse(float L) { return L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L); }
+
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(dev::pack_bf16x2(v.x, v.y), dev::pack_bf16x2(v.z, v.w));
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) cache_finish_kernel(FinishArgs a) {
+  __shared__ float4 join[8][32];
+  __shared__ float2 fin[kMaxDraft * 16];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  dev::wait_for_launches();
+
+  if ((int)blockIdx.x < a.out_ctas) {
+    // ------------------------------------------------ output rows, warps_per_row warps each
+    const int W = a.warps_per_row, part = warp % W;
+    const int64_t row = (int64_t)blockIdx.x * (8 / W) + warp / W;
+    const int h_q = a.h_kv * a.group;
+    const bool in = row < (int64_t)a.batch * h_q * a.n_q;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float L = 0.f;
+    int i = 0, b = 0, h = 0;
+    if (in) {
+      i = (int)(row % a.n_q);
+      const int bh = (int)(row / a.n_q);
+      b = bh / h_q;
+      h = bh - b * h_q;
+      const int g = h / a.group, j = h - g * a.group;
+      const Pieces p = find_pieces(a, b, g, i, j);
+      const float2 st = row_stats(a, p, lane);
+      L = st.y;
+      const int n = p.count[0] + p.count[1];
+      for (int i0 = 0; i0 < n; i0 += 32) {
+        float w = 0.f;
+        if (i0 + lane < n) w = exp2f(piece_ml(a, p, i0 + lane).x - st.x);
+        const int m = n - i0 < 32 ? n - i0 : 32;
+#pragma unroll 4
+        for (int c = part; c < m; c += W) {
+          const float f = __shfl_sync(0xffffffffu, w, c);
+          if (f == 0.f) continue;   // nothing of the piece counts (it may not even be written)
+          const int q = i0 + c;
+          const bool own = q < p.count[0];
+          const PartSrc& s = own ? a.main : a.pre;
+          const int64_t at = p.at[own ? 0 : 1] + (int64_t)(own ? q : q - p.count[0]) * s.block;
+          const float4 x = *reinterpret_cast<const float4*>(s.o + at * kHeadDim + lane * 4);
+          o.x += f * x.x, o.y += f * x.y, o.z += f * x.z, o.w += f * x.w;
+        }
+      }
+    }
+    if (W > 1) {
+      join[warp][lane] = o;
+      __syncthreads();
+      if (part == 0)
+        for (int c = 1; c < W; ++c) {
+          const float4 x = join[warp + c][lane];
+          o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
+        }
+    }
+    if (in && part == 0) {
+      const float inv = inverse(L);
+      T* dst = static_cast<T*>(a.out) + b * a.so.seq + h * a.so.head + i * a.so.token;
+      store4(dst + lane * 4, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+    }
+    return;
+  }
+  // ------------------------------------------------ scores: one thread per key, the rows in order
+  const int id = blockIdx.x - a.out_ctas;
+  const int unit = id / a.score_ctas, b = unit / a.h_kv, g = unit - b * a.h_kv;
+  const KeyList list = key_list(dev::clamp_len(a.kv_len, b, a.n_k), a.n_q, 0, a.n_q - 1, a.window, a.sinks);
+  const int stride = a.score_ctas * kThreads * kScoreKeys;
+  int u = (id - unit * a.score_ctas) * kThreads * kScoreKeys;
+  if (u >= list.total) return;
+  const int rows = a.n_q * a.group;
+  for (int r = warp; r < rows; r += 8) {
+    const float2 st = row_stats(a, find_pieces(a, b, g, r / a.group, r % a.group), lane);
+    if (lane == 0) fin[r] = make_float2(st.x, inverse(st.y));
+  }
+  __syncthreads();
+  for (u += threadIdx.x; u < list.total; u += stride) {
+    const float* x = a.logits + (int64_t)unit * rows * a.pitch + u;
+    float sum[kScoreKeys], old[kScoreKeys];
+    int at[kScoreKeys];   // offsets that stay inside the list
+    float* dst = a.score + (int64_t)unit * a.n_k;
+#pragma unroll
+    for (int c = 0; c < kScoreKeys; ++c) {
+      sum[c] = 0.f;
+      at[c] = u + c * kThreads < list.total ? c * kThreads : -1;
+      old[c] = at[c] >= 0 ? dst[list.key(u + at[c])] : 0.f;
+    }
+    for (int r = 0; r < rows; r += kScoreRows) {
+      float y[kScoreRows][kScoreKeys];   // all loads of a step before any arithmetic
+#pragma unroll
+      for (int q = 0; q < kScoreRows; ++q)
+#pragma unroll
+        for (int c = 0; c < kScoreKeys; ++c)
+          y[q][c] = at[c] >= 0 && r + q < rows ? __ldcs(x + (r + q) * a.pitch + at[c]) : -INFINITY;
+#pragma unroll
+      for (int q = 0; q < kScoreRows; ++q) {
+        const float2 f = fin[r + q < rows ? r + q : r];
+#pragma unroll
+        for (int c = 0; c < kScoreKeys; ++c) {
+          const float w = dev::ex2(y[q][c] - f.x) * f.y;
+          sum[c] += y[q][c] == -INFINITY ? 0.f : w;   // -inf: the row does not see the key
+        }
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < kScoreKeys; ++c)
+      if (at[c] >= 0) dst[list.key(u + at[c])] = old[c] + sum[c];
+  }
 }
 
 }  // namespace
 
-cudaError_t launch_cache_merge(const MergeArgs& a, cudaStream_t st) {
+cudaError_t launch_cache_finish(const FinishArgs& args, cudaStream_t st) {
+  FinishArgs a = args;
   const int64_t rows = (int64_t)a.batch * a.h_kv * a.group * a.n_q;
-  if (rows > INT32_MAX) return cudaErrorInvalidValue;
-  if (a.fp32)
-    cache_merge_kernel<float><<<(unsigned)rows, kHeadDim, 0, st>>>(a);
-  else
-    cache_merge_kernel<__nv_bfloat16><<<(unsigned)rows, kHeadDim, 0, st>>>(a);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_cache_score(const ScoreArgs& a, cudaStream_t st) {
-  const int64_t most = (int64_t)a.sinks + a.window + a.n_q - 1;
-  const int keys = most < a.n_k ? (int)most : a.n_k;
-  const dim3 grid((keys + 255) / 256, a.batch * a.h_kv);
-  cache_score_kernel<<<grid, 256, a.n_q * a.group * sizeof(float2), st>>>(a);
-  return cudaGetLastError();
+  const int64_t per_cta = 8 / a.warps_per_row;
+  const int64_t out_ctas = (rows + per_cta - 1) / per_cta;
+  int64_t score_ctas = 0;
+  if (a.logits != nullptr) {
+    const int64_t most = (int64_t)a.sinks + a.window + a.n_q - 1;
+    const int64_t keys = most < a.n_k ? most : a.n_k;
+    score_ctas = (keys + kThreads * kScoreKeys - 1) / (kThreads * kScoreKeys);
+    // about four CTAs per SM, each going through its share of a unit's keys:
+    // the row statistics that every CTA computes are a few us
+    const int64_t most_ctas = 592 / ((int64_t)a.batch * a.h_kv);
+    score_ctas = score_ctas < most_ctas ? score_ctas : (most_ctas > 1 ? most_ctas : 1);
+  }
+  const int64_t grid = out_ctas + score_ctas * a.batch * a.h_kv;
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  a.out_ctas = (int)out_ctas;
+  a.score_ctas = (int)score_ctas;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return a.fp32 ? cudaLaunchKernelEx(&cfg, cache_finish_kernel<float>, a)
+                : cudaLaunchKernelEx(&cfg, cache_finish_kernel<__nv_bfloat16>, a);
 }
 
 }  // namespace crisp
