@@ -252,8 +252,9 @@ struct CachePlan {
 CachePlan plan_cache(const CacheShape& s, int op);
 
 // ---- launchers (each enqueues on `st`; return cudaGetLastError()) ----
+cudaError_t launch_cache_tc(const CacheArgs& a, const AttnPlan& p, cudaStream_t st);
 cudaError_t launch_cache_decode(const CacheArgs& a, const AttnPlan& p, cudaStream_t st);
-cudaError_t launch_cache_tile(const CacheArgs& a, const AttnPlan& p, bool fp32, cudaStream_t st);
+cudaError_t launch_cache_tile(const CacheArgs& a, const AttnPlan& p, cudaStream_t st);   // fp32
 
 struct FinishArgs {
   PartSrc main, pre;

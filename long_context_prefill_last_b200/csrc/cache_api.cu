@@ -137,6 +137,22 @@ AttnPlan plan_tile(int units, int rows, int keys) {
   return p;
 }
 
+// Grid of the tcgen05 kernel: one CTA per SM; key lists are split while that
+// fills more SMs, with at least two key tiles in each split.
+AttnPlan plan_tc(int units, int rows, int keys) {
+  AttnPlan p{};
+  p.kernel = kTileTc;
+  p.units = units;
+  p.tile = 128;
+  p.block = 256;
+  p.blocks = (rows + 255) / 256;
+  const int64_t jobs = (int64_t)units * p.blocks;
+  const int tiles = (keys + 127) / 128;
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(kSms / jobs, tiles / 2));
+  p.slots = (size_t)jobs * p.splits;
+  return p;
+}
+
 // Grid of the bf16 decode kernel: two CTAs per SM, or one per key tile when
 // there are fewer.
 AttnPlan plan_decode(int units, int rows, int keys) {
@@ -169,16 +185,19 @@ CachePlan plan_cache(const CacheShape& s, int op) {
   };
   if (op != CRISP_CACHE_EVICT) {
     const int units = s.batch * s.h_kv, rows = s.n_q * s.group;
-    const int64_t seen = (int64_t)s.window + s.sinks + s.n_q - 1;
+    // keys that one CTA's rows can span: tokens in its rows, the window and the first keys
+    const int tokens = std::min(s.n_q, s.fp32 ? 64 : 256);
+    const int64_t seen = (int64_t)s.window + s.sinks + tokens - 1;
     const int keys = (int)std::min<int64_t>(s.n_k, seen);
     p.has_pre = op == CRISP_CACHE_PREFIX;
-    // bf16 drafts take the decode kernel, as does a prefix read by at most 64 rows
-    const bool draft = !s.fp32 && s.n_q <= kMaxDraft;
-    p.main = draft ? plan_decode(units, rows, keys) : plan_tile(units, rows, keys);
-    if (p.has_pre) {
-      const int all = s.batch * rows;
-      p.pre = !s.fp32 && all <= 64 ? plan_decode(s.h_kv, all, s.n_prefix) : plan_tile(s.h_kv, all, s.n_prefix);
-    }
+    // fp32: the CUDA-core tiles; bf16: drafts, and a prefix that at most 64 rows
+    // read, take the decode kernel, more rows the tcgen05 tiles
+    auto plan = [&](int n_units, int n_rows, int n_keys, bool few) {
+      return s.fp32 ? plan_tile(n_units, n_rows, n_keys)
+                    : few ? plan_decode(n_units, n_rows, n_keys) : plan_tc(n_units, n_rows, n_keys);
+    };
+    p.main = plan(units, rows, keys, s.n_q <= kMaxDraft);
+    if (p.has_pre) p.pre = plan(s.h_kv, s.batch * rows, s.n_prefix, s.batch * rows <= 64);
     // output rows straight away when no row's keys are split
     if (op == CRISP_CACHE_WINDOW && p.main.kernel != kDecodeMma && p.main.splits == 1) p.main.slots = 0;
     // a row's pieces are read by one warp while there are few, by up to eight when there are many
@@ -216,7 +235,9 @@ crisp_status run_attention(const void* q, const void* kp, const void* vp, const 
   const bool clear = p.main.kernel != kDecodeMma || (p.has_pre && p.pre.kernel != kDecodeMma);
   if (clear) CACHE_TRY(cudaMemsetAsync(status, 0, 32, st));
   auto launch = [&](const AttnPlan& pl, const CacheArgs& a) {
-    return pl.kernel == kDecodeMma ? launch_cache_decode(a, pl, st) : launch_cache_tile(a, pl, s.fp32, st);
+    return pl.kernel == kDecodeMma ? launch_cache_decode(a, pl, st)
+           : pl.kernel == kTileTc ? launch_cache_tc(a, pl, st)
+                                  : launch_cache_tile(a, pl, st);
   };
   CacheArgs a{};
   a.q = q;

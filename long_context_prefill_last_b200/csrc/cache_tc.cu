@@ -1,0 +1,527 @@
+// Attention over a key/value cache on the 5th-generation tensor cores
+// (tcgen05.mma, accumulators in TMEM, keys and values staged by TMA), bf16:
+// prompts and appended chunks through a window, and a prefix shared by many
+// rows. For query row r at position p and the keys j it sees (0 <= j <= p,
+// and j < sinks or j > p - window), in one pass over the keys:
+//     o_r = sum_j 2^(x_rj - m_r) v_j / l_r,   x_rj = scale * log2(e) * q_r . k_j
+//
+// Bound: the tensor pipe (4 * 128 FLOP per row and key) beside the softmax's
+// issue slots. One CTA takes 256 rows of a unit (tiles A and B of 128) and a
+// range of its key tiles. A row is a (token, head of the group) pair, so the
+// query heads that share a key/value head read its tiles once, and the keys
+// that 256 rows span beyond the window are few (64 tokens at 4 heads a group).
+// Key tiles start at the first key that the CTA's rows see, wherever that is:
+// TMA boxes need no alignment along the tokens.
+//
+// Warps, TMEM columns, register split and MMA order follow attn_tc.cu:
+//   warp 0       TMA producer: K (3-stage ring), V (2-stage ring); clears the
+//                V rows behind the last key of a list segment, whose weights
+//                are zero but whose content may be anything
+//   warp 1       TMEM allocation; one elected lane issues every tcgen05.mma
+//   warps 4..7   softmax of tile A, warps 8..11 of tile B (row = TMEM lane)
+// TMEM: S_A [0,128), S_B [128,256), O_A [256,384), O_B [384,512); P (bf16)
+// over the first 64 columns of S. Issue order per key tile u:
+//     S_B(u) = Q_B K_u^T,  O_A += P_A(u) V_u,  S_A(u+1) = Q_A K_{u+1}^T,  O_B += P_B(u) V_u
+// S_X(u) landing means O_X already holds P_X(u-1) V, so a softmax warp may
+// rescale O_X then; it does when a row's maximum grew by more than 2^8.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cudaTypedefs.h>
+
+#include "cache.h"
+#include "ptx.cuh"
+#include "tmap.h"
+
+namespace crisp {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kRegsControl = 64;
+constexpr int kRegsSoftmax = 216;
+static_assert(128 * kRegsControl + 256 * kRegsSoftmax <= kThreads * 168, "register split exceeds the launch");
+constexpr int kKStages = 3;
+constexpr int kVStages = 2;
+constexpr uint32_t kTileBytes = 128 * 128 * 2;   // a bf16 128x128 tile: two 64-column halves
+constexpr uint32_t kHalfBytes = 128 * 128;       // 128 rows x 128 bytes
+constexpr uint32_t OFF_Q = 0;                    // A, then B
+constexpr uint32_t OFF_K = 2 * kTileBytes;
+constexpr uint32_t OFF_V = OFF_K + kKStages * kTileBytes;
+constexpr uint32_t OFF_BAR = OFF_V + kVStages * kTileBytes;
+enum {
+  B_KFULL = 0,
+  B_KEMPTY = B_KFULL + kKStages,
+  B_VFULL = B_KEMPTY + kKStages,
+  B_VEMPTY = B_VFULL + kVStages,
+  B_VCLEAR = B_VEMPTY + kVStages,  // the rows behind a segment's end are zero (one arrival per tile)
+  B_SFULL = B_VCLEAR + kVStages,   // [2]: S_X landed
+  B_PFULL = B_SFULL + 2,           // [2]: P_X written (128 arrivals)
+  B_DONE = B_PFULL + 2,            // [2]: last P_X V landed
+  B_DRAIN = B_DONE + 2,
+  B_COUNT = B_DRAIN + 1
+};
+constexpr uint32_t OFF_TMEMPTR = OFF_BAR + 8 * B_COUNT;
+constexpr uint32_t OFF_ABORT = OFF_TMEMPTR + 4;
+constexpr uint32_t kSmemBytes = OFF_ABORT + 4 + 1024;   // + slack to align the base to 1024
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+constexpr uint32_t kTmemCols = 512;
+constexpr float kRescaleLog2 = 8.f;
+
+__device__ __forceinline__ uint32_t bar_addr(uint32_t base, int i) { return base + OFF_BAR + 8u * i; }
+
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int32_t* status,
+                                          int where) {
+  const bool ok = dev::mbar_wait(bar, parity, abort_flag, status, where);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// 4-D tiled load (d, token, head, sequence); x is a multiple of 64 elements.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint32_t bar, int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
+      ::"r"(dst), "l"(tmap), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+
+enum Kind : int { kNone = 0, kWhole = 1, kPart = 2 };
+
+// The CTA's key tiles: those of the first keys [0, se), then those of [lo, hi).
+struct Sched {
+  int se, lo, hi, sink_tiles, t0, t1;
+  int window, sinks;
+  int first[2], last[2];   // positions of the first and last row of A and B (B absent: last < 0)
+  __device__ int key0(int t) const { return t < sink_tiles ? t * 128 : lo + (t - sink_tiles) * 128; }
+  __device__ int end(int t) const {   // one past the tile's last key
+    const int k = key0(t) + 128, e = t < sink_tiles ? se : hi;
+    return k < e ? k : e;
+  }
+  __device__ int kind(int x, int t) const {
+    const int k0 = key0(t), k1 = end(t);
+    if (k0 > last[x] || (k0 >= sinks && k1 - 1 <= first[x] - window)) return kNone;
+    if (k1 - k0 == 128 && k1 - 1 <= first[x] && (k0 > last[x] - window || k1 <= sinks)) return kWhole;
+    return kPart;
+  }
+  // next tile >= t that A or B needs; false at the end
+  __device__ bool next(int& t, int& ka, int& kb) const {
+    for (; t < t1; ++t) {
+      ka = kind(0, t);
+      kb = kind(1, t);
+      if (ka != kNone || kb != kNone) return true;
+    }
+    return false;
+  }
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+cache_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, CacheArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = dev::smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  uint8_t* sgen = smem_raw + (sbase - raw);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sgen + OFF_ABORT);
+  uint32_t* tmem_ptr_smem = reinterpret_cast<uint32_t*>(sgen + OFF_TMEMPTR);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  const int split = blockIdx.x % a.splits;
+  const int job = blockIdx.x / a.splits;
+  const int pair = job % a.blocks, unit = job / a.blocks;
+  const int b = unit / a.h_kv, g = unit - b * a.h_kv;
+  const int len = dev::cache_len(a, b);
+  const int r0 = pair * 256;
+  const bool hasB = r0 + 128 < a.rows;
+
+  Sched sc;
+  {
+    const int r_last = (r0 + 256 < a.rows ? r0 + 256 : a.rows) - 1;
+    const KeyList list = dev::unit_keys(a, len, r0 / a.group, r_last / a.group);
+    sc.se = list.se;
+    sc.lo = list.lo;
+    sc.hi = list.lo + (list.total - list.se);
+    if (sc.lo <= sc.se) {   // the window begins at the end of the first keys: one segment
+      sc.se = 0;
+      sc.lo = 0;
+    }
+    sc.sink_tiles = (sc.se + 127) / 128;
+    const int tiles = sc.sink_tiles + (sc.hi - sc.lo + 127) / 128;
+    sc.t0 = (int)((int64_t)tiles * split / a.splits);
+    sc.t1 = (int)((int64_t)tiles * (split + 1) / a.splits);
+    sc.window = a.window;
+    sc.sinks = a.sinks;
+    const int a_last = hasB ? r0 + 127 : r_last;
+    sc.first[0] = dev::row_pos(a, len, r0 / a.group);
+    sc.last[0] = dev::row_pos(a, len, a_last / a.group);
+    sc.first[1] = hasB ? dev::row_pos(a, len, (r0 + 128) / a.group) : -1;
+    sc.last[1] = hasB ? dev::row_pos(a, len, r_last / a.group) : -1;
+  }
+
+  if (threadIdx.x == 0) {
+    *abort_flag = dev::load_volatile(a.status) != 0 ? 1 : 0;   // an earlier failure: do nothing
+    for (int s = 0; s < kKStages; ++s) {
+      dev::mbar_init(bar_addr(sbase, B_KFULL + s), 1);
+      dev::mbar_init(bar_addr(sbase, B_KEMPTY + s), 1);
+    }
+    for (int s = 0; s < kVStages; ++s) {
+      dev::mbar_init(bar_addr(sbase, B_VFULL + s), 1);
+      dev::mbar_init(bar_addr(sbase, B_VEMPTY + s), 1);
+      dev::mbar_init(bar_addr(sbase, B_VCLEAR + s), 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      dev::mbar_init(bar_addr(sbase, B_SFULL + x), 1);
+      dev::mbar_init(bar_addr(sbase, B_PFULL + x), 128);
+      dev::mbar_init(bar_addr(sbase, B_DONE + x), 1);
+    }
+    dev::mbar_init(bar_addr(sbase, B_DRAIN), 1);
+    dev::fence_mbar_init();
+  }
+  // queries: 16-byte pieces into the 128-byte swizzled layout; rows past the unit's end are zero
+  for (int e = threadIdx.x; e < 256 * 16; e += kThreads) {
+    const int r = e >> 4, c = e & 15;
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    if (r0 + r < a.rows) {
+      const dev::Row w = dev::unit_row(a, b, g, r0 + r);
+      x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + w.b * a.sq.seq + w.h * a.sq.head +
+                                          w.i * a.sq.token + c * 8);
+    }
+    const uint32_t off = OFF_Q + (r >> 7) * kTileBytes + (c >> 3) * kHalfBytes + (r & 127) * 128 +
+                         (((c & 7) ^ (r & 7)) << 4);
+    *reinterpret_cast<uint4*>(sgen + off) = x;
+  }
+  dev::fence_proxy_async_smem();
+  __syncthreads();
+  if (*abort_flag) return;   // uniform: read after the barrier, before any TMEM is taken
+  if (warp == 1) {
+    dev::tmem_alloc(dev::smem_u32(tmem_ptr_smem), kTmemCols);
+    dev::tmem_relinquish();
+  }
+  dev::tc_fence_before();
+  __syncthreads();
+  dev::tc_fence_after();
+  const uint32_t tmem = *tmem_ptr_smem;
+
+  if (warp < 4) dev::regs_release<kRegsControl>();
+  if (warp == 0) {
+    // ---------------------------------------------------------------- TMA producer
+    if (lane == 0) {
+      dev::prefetch_tmap(&tm_k);
+      dev::prefetch_tmap(&tm_v);
+    }
+    int u = 0, t = sc.t0, ka = 0, kb = 0, prev_t = -1;
+    int issued_k = 0, issued_v = 0;
+    bool ok = true, more = true;
+    while (ok && (more || prev_t >= 0)) {
+      more = more && sc.next(t, ka, kb);
+      if (more) {   // K of tile u
+        const int s = u % kKStages;
+        if (!warp_wait(bar_addr(sbase, B_KEMPTY + s), ((u / kKStages) & 1) ^ 1, abort_flag, a.status, 1)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          const uint32_t bk = bar_addr(sbase, B_KFULL + s);
+          dev::mbar_arrive_expect_tx(bk, kTileBytes);
+          tma_load_4d(sbase + OFF_K + s * kTileBytes, &tm_k, bk, 0, sc.key0(t), g, b);
+          tma_load_4d(sbase + OFF_K + s * kTileBytes + kHalfBytes, &tm_k, bk, 64, sc.key0(t), g, b);
+        }
+        ++issued_k;
+      }
+      if (prev_t >= 0) {   // V of tile u-1
+        const int uv = u - 1, s = uv % kVStages;
+        const uint32_t vbase = OFF_V + s * kTileBytes, bv = bar_addr(sbase, B_VFULL + s);
+        if (!warp_wait(bar_addr(sbase, B_VEMPTY + s), ((uv / kVStages) & 1) ^ 1, abort_flag, a.status, 2)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          dev::mbar_arrive_expect_tx(bv, kTileBytes);
+          tma_load_4d(sbase + vbase, &tm_v, bv, 0, sc.key0(prev_t), g, b);
+          tma_load_4d(sbase + vbase + kHalfBytes, &tm_v, bv, 64, sc.key0(prev_t), g, b);
+        }
+        ++issued_v;
+        const int valid = sc.end(prev_t) - sc.key0(prev_t);
+        if (valid < 128) {   // rows behind the segment's end: whatever the cache holds there, 0 * x has to be 0
+          if (!warp_wait(bv, (uv / kVStages) & 1, abort_flag, a.status, 9)) {
+            ok = false;
+            break;
+          }
+          for (int e = lane; e < (128 - valid) * 16; e += 32) {
+            const int row = valid + (e >> 4), c = e & 15;
+            *reinterpret_cast<uint4*>(sgen + vbase + (c >> 3) * kHalfBytes + row * 128 + (c & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+          }
+          dev::fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (lane == 0) dev::mbar_arrive(bar_addr(sbase, B_VCLEAR + s));
+      }
+      prev_t = more ? t : -1;
+      if (more) {
+        ++t;
+        ++u;
+      }
+    }
+    if (!ok) {
+      // error path: let the copies already issued land before the CTA exits
+      for (int s = 0; s < kKStages && s < issued_k; ++s) {
+        const int last = issued_k - 1 - ((issued_k - 1 - s) % kKStages);
+        dev::mbar_drain(bar_addr(sbase, B_KFULL + s), (last / kKStages) & 1);
+      }
+      for (int s = 0; s < kVStages && s < issued_v; ++s) {
+        const int last = issued_v - 1 - ((issued_v - 1 - s) % kVStages);
+        dev::mbar_drain(bar_addr(sbase, B_VFULL + s), (last / kVStages) & 1);
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer
+    const uint32_t idesc_qk = dev::umma_idesc_bf16(128, 128, false);
+    const uint32_t idesc_pv = dev::umma_idesc_bf16(128, 128, true);
+    const uint64_t QD0 = dev::smem_desc_sw128(sbase + OFF_Q, 16, 1024);
+    const uint64_t KD0 = dev::smem_desc_sw128(sbase + OFF_K, 16, 1024);
+    const uint64_t VD0 = dev::smem_desc_sw128(sbase + OFF_V, kHalfBytes, 1024);
+    int kx0 = 0, kx1 = 0;   // P.V issued per row tile
+    auto qk = [&](int x, int u) {
+      dev::umma_ss8_w(tmem + (uint32_t)x * 128u, QD0 + (uint64_t)(x * (kTileBytes >> 4)),
+                      KD0 + (uint64_t)((u % kKStages) * (kTileBytes >> 4)), idesc_qk, 0u);
+      dev::umma_commit_w(bar_addr(sbase, B_SFULL + x));
+    };
+    auto pv = [&](int x, int u) -> bool {
+      const int kx = x == 0 ? kx0 : kx1;
+      if (!warp_wait(bar_addr(sbase, B_PFULL + x), kx & 1, abort_flag, a.status, 4 + x)) return false;
+      dev::tc_fence_after();
+      dev::umma_ts8_w(tmem + 256u + (uint32_t)x * 128u, tmem + (uint32_t)x * 128u,
+                      VD0 + (uint64_t)((u % kVStages) * (kTileBytes >> 4)), idesc_pv, kx > 0 ? 1u : 0u);
+      if (x == 0) ++kx0; else ++kx1;
+      return true;
+    };
+    int t = sc.t0, ka = 0, kb = 0;
+    bool ok = true;
+    bool have = sc.next(t, ka, kb);
+    if (have) {
+      ok = warp_wait(bar_addr(sbase, B_KFULL + 0), 0, abort_flag, a.status, 6);
+      dev::tc_fence_after();
+      if (ok && ka != kNone) qk(0, 0);
+    }
+    int u = 0;
+    while (ok && have) {
+      if (kb != kNone) qk(1, u);
+      dev::umma_commit_w(bar_addr(sbase, B_KEMPTY + u % kKStages));
+      int t2 = t + 1, ka2 = 0, kb2 = 0;
+      const bool have2 = sc.next(t2, ka2, kb2);
+      if (!warp_wait(bar_addr(sbase, B_VFULL + u % kVStages), (u / kVStages) & 1, abort_flag, a.status, 7) ||
+          !warp_wait(bar_addr(sbase, B_VCLEAR + u % kVStages), (u / kVStages) & 1, abort_flag, a.status, 3)) {
+        ok = false;
+        break;
+      }
+      dev::tc_fence_after();
+      if (ka != kNone && !pv(0, u)) {
+        ok = false;
+        break;
+      }
+      if (have2) {
+        if (!warp_wait(bar_addr(sbase, B_KFULL + (u + 1) % kKStages), ((u + 1) / kKStages) & 1, abort_flag, a.status,
+                       8)) {
+          ok = false;
+          break;
+        }
+        dev::tc_fence_after();
+        if (ka2 != kNone) qk(0, u + 1);
+      }
+      if (kb != kNone && !pv(1, u)) {
+        ok = false;
+        break;
+      }
+      dev::umma_commit_w(bar_addr(sbase, B_VEMPTY + u % kVStages));
+      t = t2;
+      ka = ka2;
+      kb = kb2;
+      have = have2;
+      ++u;
+    }
+    if (ok) {
+      dev::umma_commit_w(bar_addr(sbase, B_DONE + 0));
+      dev::umma_commit_w(bar_addr(sbase, B_DONE + 1));
+    }
+    // every MMA issued must complete before TMEM is released
+    dev::umma_commit_w(bar_addr(sbase, B_DRAIN));
+    dev::mbar_drain(bar_addr(sbase, B_DRAIN), 0);
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ---------------------------------------------------------------- softmax warps
+    dev::regs_acquire<kRegsSoftmax>();
+    const int x = (warp - 4) >> 2;                // 0: tile A, 1: tile B
+    const int quarter = warp & 3;                 // TMEM lane quarter of this warp
+    const int r = quarter * 32 + lane;            // row inside the tile
+    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    const uint32_t s_col = tmem + lane_base + (uint32_t)x * 128;
+    const uint32_t o_col = tmem + lane_base + 256u + (uint32_t)x * 128;
+    const int row = r0 + x * 128 + r;
+    if (x == 0 || hasB) {
+      const bool in = row < a.rows;
+      const dev::Row w = dev::unit_row(a, b, g, in ? row : 0);
+      const int pos = in ? dev::row_pos(a, len, w.i) : -1;
+      const float sl2 = a.scale_log2;
+      float m_ref = -INFINITY, l = 0.f;
+      int k = 0;
+      bool ok = true;
+      for (int t = sc.t0; t < sc.t1; ++t) {
+        const int kind = sc.kind(x, t);
+        if (kind == kNone) continue;
+        if (!warp_wait(bar_addr(sbase, B_SFULL + x), k & 1, abort_flag, a.status, 10 + x)) {
+          ok = false;
+          break;
+        }
+        dev::tc_fence_after();
+        float s[128];
+        dev::tmem_ld128(s_col, s);
+        dev::tmem_wait_ld();
+        if (kind == kPart) {
+          // column c is key k0 + c: seen for low < c <= high, or c < front
+          const int k0 = sc.key0(t), e = sc.end(t) - 1;
+          const int high = (pos < e ? pos : e) - k0, low = pos - a.window - k0, front = a.sinks - k0;
+          if (front <= 0 || low < 0) {
+#pragma unroll
+            for (int c = 0; c < 128; ++c) s[c] = (c <= high && c > low) ? s[c] : -INFINITY;
+          } else {
+#pragma unroll
+            for (int c = 0; c < 128; ++c) s[c] = (c <= high && (c > low || c < front)) ? s[c] : -INFINITY;
+          }
+        }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int c = 4; c < 124; c += 8) {
+          mx[0] = dev::max3(mx[0], s[c], s[c + 1]);
+          mx[1] = dev::max3(mx[1], s[c + 2], s[c + 3]);
+          mx[2] = dev::max3(mx[2], s[c + 4], s[c + 5]);
+          mx[3] = dev::max3(mx[3], s[c + 6], s[c + 7]);
+        }
+        mx[0] = dev::max3(mx[0], s[124], s[125]);
+        mx[1] = dev::max3(mx[1], s[126], s[127]);
+        const float tmax = fmaxf(dev::max3(mx[0], mx[1], mx[2]), mx[3]) * sl2;
+        const bool need = tmax > m_ref + kRescaleLog2 || (m_ref == -INFINITY && tmax > -INFINITY);
+        const float factor = need ? dev::ex2(m_ref - tmax) : 1.f;   // 0 when m_ref = -inf
+        if (k > 0 && __any_sync(0xffffffffu, need)) {
+          // O holds P V of every earlier tile (it completed before S landed)
+#pragma unroll 1
+          for (int c0 = 0; c0 < 128; c0 += 32) {
+            uint32_t v[32];
+            dev::tmem_ld32(o_col + c0, v);
+            dev::tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * factor);
+            dev::tmem_st32(o_col + c0, v);
+          }
+        }
+        if (need) {
+          l *= factor;
+          m_ref = tmax;
+        }
+        const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
+        // P = 2^(x - m), rounded to bf16 for the product with V (l keeps it in
+        // fp32); chunk c0 goes to S columns [c0/2, c0/2 + 16), already consumed
+        const uint64_t scale2 = dev::f2_pack(sl2, sl2), negm2 = dev::f2_pack(neg_m, neg_m);
+        uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+        for (int c0 = 0; c0 < 128; c0 += 32) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const int c = c0 + 2 * j;
+            const uint64_t x2 = dev::f2_fma(dev::f2_pack(s[c], s[c + 1]), scale2, negm2);
+            float x0, x1;
+            dev::f2_unpack(x2, x0, x1);
+            const float p0 = dev::ex2(x0), p1 = dev::ex2(x1);
+            acc[j & 3] = dev::f2_add(acc[j & 3], dev::f2_pack(p0, p1));
+            pk[j] = dev::pack_bf16x2(p0, p1);
+          }
+          dev::tmem_st16(s_col + (c0 >> 1), pk);
+        }
+        float sum[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dev::f2_unpack(acc[j], sum[2 * j], sum[2 * j + 1]);
+        dev::tmem_wait_st();
+        dev::tc_fence_before();
+        dev::mbar_arrive(bar_addr(sbase, B_PFULL + x));
+        l += ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7]));
+        ++k;
+      }
+      if (ok && k > 0) {
+        ok = warp_wait(bar_addr(sbase, B_DONE + x), 0, abort_flag, a.status, 12 + x);
+        dev::tc_fence_after();
+      }
+      if (ok && a.part_o != nullptr) {
+        const int64_t at = ((int64_t)job * a.splits + split) * 256 + x * 128 + r;
+        if (in) a.part_ml[at] = make_float2(m_ref, l);
+        if (k > 0) {   // without a key tile the piece has weight 0 and is not read
+          float* dst = a.part_o + at * kHeadDim;
+#pragma unroll
+          for (int c0 = 0; c0 < 128; c0 += 32) {
+            uint32_t v[32];
+            dev::tmem_ld32(o_col + c0, v);
+            dev::tmem_wait_ld();
+            if (in) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<uint4*>(dst + c0 + 4 * j) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            }
+          }
+        }
+      } else if (ok) {
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // no key: 0; NaN stays NaN
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + w.b * a.so.seq + w.h * a.so.head + w.i * a.so.token;
+#pragma unroll
+        for (int c0 = 0; c0 < 128; c0 += 32) {
+          uint32_t v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = 0u;
+          if (k > 0) {
+            dev::tmem_ld32(o_col + c0, v);
+            dev::tmem_wait_ld();
+          }
+          if (in) {
+            uint32_t y[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              y[j] = dev::pack_bf16x2(__uint_as_float(v[2 * j]) * inv, __uint_as_float(v[2 * j + 1]) * inv);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<uint4*>(dst + c0 + 8 * j) = make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+          }
+        }
+      }
+    }
+    dev::tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 1) {
+    dev::tc_fence_after();
+    dev::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Boxes of 64 columns (128 bytes) x 128 tokens of one head, 128-byte swizzle.
+bool make_cache_map(CUtensorMap* m, const void* ptr, int n, int heads, int seqs, const Strides& s) {
+  auto fn = tmap_encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {(cuuint64_t)kHeadDim, (cuuint64_t)n, (cuuint64_t)heads, (cuuint64_t)seqs};
+  cuuint64_t strides[3] = {(cuuint64_t)s.token * 2, (cuuint64_t)s.head * 2, (cuuint64_t)s.seq * 2};
+  cuuint32_t box[4] = {64, 128, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+cudaError_t launch_cache_tc(const CacheArgs& a, const AttnPlan& p, cudaStream_t st) {
+  CUtensorMap mk, mv;
+  if (!make_cache_map(&mk, a.k, a.n_keys, a.h_kv, a.batch, a.sk) ||
+      !make_cache_map(&mv, a.v, a.n_keys, a.h_kv, a.batch, a.sv))
+    return cudaErrorInvalidValue;
+  const int64_t grid = (int64_t)p.units * p.blocks * p.splits;
+  if (grid <= 0 || grid > INT32_MAX) return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(cache_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return e;
+  cache_tc_kernel<<<(unsigned)grid, kThreads, kSmemBytes, st>>>(mk, mv, a);
+  return cudaGetLastError();
+}
+
+}  // namespace crisp

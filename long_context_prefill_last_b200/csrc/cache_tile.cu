@@ -10,7 +10,6 @@
 // tx + 16 j, and output columns 4 tx .. 4 tx + 3 and 64 + 4 tx .. of the same
 // rows. A row of a unit is a (token, head of the group) pair, so a key tile is
 // read once for all query heads that share it.
-#include <cuda_bf16.h>
 #include <math.h>
 
 #include "cache.h"
@@ -25,24 +24,9 @@ constexpr int kPitch = kHeadDim + 4;      // floats per staged Q or K row: 16 ro
 constexpr int kPPitch = kRows + 4;        // floats per key of the staged probabilities
 constexpr int kSmem = (2 * kRows * kPitch + kKeys * kHeadDim) * 4;
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const T* p);
-template <>
-__device__ __forceinline__ float4 load4<float>(const float* p) {
-  return *reinterpret_cast<const float4*>(p);
-}
-template <>
-__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
-  const uint2 w = *reinterpret_cast<const uint2*>(p);
-  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                     __uint_as_float(w.y & 0xffff0000u));
-}
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(dev::pack_bf16x2(v.x, v.y), dev::pack_bf16x2(v.z, v.w));
-}
 
-template <typename T>
 __global__ void __launch_bounds__(256, 2) cache_tile_kernel(CacheArgs a) {
   extern __shared__ __align__(16) float sm[];
   float* qs = sm;
@@ -68,7 +52,7 @@ __global__ void __launch_bounds__(256, 2) cache_tile_kernel(CacheArgs a) {
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r0 + r < a.rows) {
       const dev::Row w = dev::unit_row(a, b, g, r0 + r);
-      x = load4<T>(static_cast<const T*>(a.q) + w.b * a.sq.seq + w.h * a.sq.head + w.i * a.sq.token + lane * 4);
+      x = load4(static_cast<const float*>(a.q) + w.b * a.sq.seq + w.h * a.sq.head + w.i * a.sq.token + lane * 4);
     }
     *reinterpret_cast<float4*>(qs + r * kPitch + lane * 4) = x;
   }
@@ -83,8 +67,8 @@ __global__ void __launch_bounds__(256, 2) cache_tile_kernel(CacheArgs a) {
     l[i] = 0.f;
     o[i][0] = o[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  const T* kp = static_cast<const T*>(a.k) + b * a.sk.seq + g * a.sk.head + lane * 4;
-  const T* vp = static_cast<const T*>(a.v) + b * a.sv.seq + g * a.sv.head + lane * 4;
+  const float* kp = static_cast<const float*>(a.k) + b * a.sk.seq + g * a.sk.head + lane * 4;
+  const float* vp = static_cast<const float*>(a.v) + b * a.sv.seq + g * a.sv.head + lane * 4;
 
   for (int t = t0; t < t1; ++t) {
     __syncthreads();
@@ -94,8 +78,8 @@ __global__ void __launch_bounds__(256, 2) cache_tile_kernel(CacheArgs a) {
       float4 kx = make_float4(0.f, 0.f, 0.f, 0.f), vx = kx;
       if (u < list.total) {
         const int64_t j = list.key(u);
-        kx = load4<T>(kp + j * a.sk.token);
-        vx = load4<T>(vp + j * a.sv.token);
+        kx = load4(kp + j * a.sk.token);
+        vx = load4(vp + j * a.sv.token);
       }
       *reinterpret_cast<float4*>(ks + c * kPitch + lane * 4) = kx;
       *reinterpret_cast<float4*>(vs + c * kHeadDim + lane * 4) = vx;
@@ -217,7 +201,7 @@ __global__ void __launch_bounds__(256, 2) cache_tile_kernel(CacheArgs a) {
     } else {
       const dev::Row w = dev::unit_row(a, b, g, r);
       const float inv = l[i] > 0.f ? 1.f / l[i] : (l[i] == 0.f ? 0.f : l[i]);   // no key: 0; NaN stays NaN
-      T* dst = static_cast<T*>(a.out) + w.b * a.so.seq + w.h * a.so.head + w.i * a.so.token;
+      float* dst = static_cast<float*>(a.out) + w.b * a.so.seq + w.h * a.so.head + w.i * a.so.token;
       store4(dst + tx * 4, make_float4(o[i][0].x * inv, o[i][0].y * inv, o[i][0].z * inv, o[i][0].w * inv));
       store4(dst + 64 + tx * 4, make_float4(o[i][1].x * inv, o[i][1].y * inv, o[i][1].z * inv, o[i][1].w * inv));
     }
@@ -226,13 +210,12 @@ __global__ void __launch_bounds__(256, 2) cache_tile_kernel(CacheArgs a) {
 
 }  // namespace
 
-cudaError_t launch_cache_tile(const CacheArgs& a, const AttnPlan& p, bool fp32, cudaStream_t st) {
+cudaError_t launch_cache_tile(const CacheArgs& a, const AttnPlan& p, cudaStream_t st) {
   const int64_t grid = (int64_t)p.units * p.blocks * p.splits;
   if (grid <= 0 || grid > INT32_MAX) return cudaErrorInvalidValue;
-  const auto kern = fp32 ? &cache_tile_kernel<float> : &cache_tile_kernel<__nv_bfloat16>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  cudaError_t e = cudaFuncSetAttribute(cache_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)grid, 256, kSmem, st>>>(a);
+  cache_tile_kernel<<<(unsigned)grid, 256, kSmem, st>>>(a);
   return cudaGetLastError();
 }
 
