@@ -422,7 +422,6 @@ crisp_status crisp_evict(const void* k, const void* v, const float* score, const
   if (score < score_new + units * s.n_new && score_new < score + units * s.n_k) return CRISP_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   char* ws = static_cast<char*>(cfg->workspace);
-  CACHE_TRY(cudaMemsetAsync(ws, 0, 32, st));
   EvictArgs a{};
   a.k = k;
   a.v = v;

@@ -4,16 +4,29 @@
 // budget - sinks - recent with the largest score (equal scores: the lower
 // index first; NaN below every number). The kept keys, values and scores move
 // to the new cache in their old order.
+//
+// Selection: the cut is found by a radix select on order-preserving 32-bit
+// keys (11 + 11 + 10 bits, counts in shared memory), then every warp counts
+// and writes the survivors of its own contiguous stretch. One cluster of 1 to
+// 8 CTAs per head shares the counts through distributed shared memory; a head
+// is a few hundred KB of scores, read once and kept in shared memory, so this
+// is bound by the latency of its few barriers. The move is bound by HBM.
+#include <cooperative_groups.h>
 #include <math.h>
 
 #include "cache.h"
 #include "ptx.cuh"
 
+namespace cg = cooperative_groups;
+
 namespace crisp {
 namespace {
 
 constexpr int kSelThreads = 1024;
-constexpr int kBins = 2048;   // 11 bits a level: 32 bits in three levels (11, 11, 10)
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kCachedKeys = 40960;   // keys of a CTA's stretch held in shared memory (160 KB)
+constexpr int kMoveKeys = 8;         // keys per warp of the move
 
 // Order-preserving 32-bit key of a score: -0 counts as +0, NaN as the lowest.
 __device__ __forceinline__ uint32_t score_key(float x) {
@@ -22,8 +35,8 @@ __device__ __forceinline__ uint32_t score_key(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Exclusive prefix sum of one value per thread over the CTA; *total gets the sum.
-__device__ __forceinline__ int cta_scan(int x, int* warp_sums, int* total) {
+// Exclusive prefix sum of one value per thread over the CTA.
+__device__ __forceinline__ int cta_scan(int x, int* warp_sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int inc = x;
 #pragma unroll
@@ -31,144 +44,261 @@ __device__ __forceinline__ int cta_scan(int x, int* warp_sums, int* total) {
     const int y = __shfl_up_sync(0xffffffffu, inc, d);
     if (lane >= d) inc += y;
   }
+  __syncthreads();
   if (lane == 31) warp_sums[warp] = inc;
   __syncthreads();
-  if (warp == 0) {
-    int w = lane < (int)(blockDim.x >> 5) ? warp_sums[lane] : 0;
+  int w = warp_sums[lane];
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, w, d);
-      if (lane >= d) w += y;
-    }
-    warp_sums[lane] = w;
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, w, d);
+    if (lane >= d) w += y;
   }
-  __syncthreads();
-  const int before = warp == 0 ? 0 : warp_sums[warp - 1];
-  *total = warp_sums[31];
-  __syncthreads();
-  return before + inc - x;
+  const int before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+  return (warp == 0 ? 0 : before) + inc - x;
 }
 
-// One CTA per (sequence, key/value head): the indices that stay, ascending.
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) {
-  __shared__ int hist[kBins];
+// One cluster per (sequence, key/value head): the indices that stay, ascending.
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a, int cs) {
+  extern __shared__ uint32_t cached[];
+  __shared__ int hist[3][kBins];
   __shared__ int warp_sums[32];
   __shared__ uint32_t found_bin;
   __shared__ int found_above;
-  const int unit = blockIdx.x, b = unit / a.h_kv, tid = threadIdx.x;
-  int len = a.kv_len != nullptr ? a.kv_len[b] : a.n_k;
-  if (len < 0 || len > a.n_k) {
-    if (tid == 0) a.status[kStatusLen] = CRISP_ERR_INVALID_ARG;
-    len = len < 0 ? 0 : a.n_k;
+  __shared__ int warp_above[kSelWarps], warp_ties[kSelWarps];
+  __shared__ int cta_counts[2];   // above the cut, equal to it
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int unit = blockIdx.x / cs, rank = blockIdx.x - unit * cs, b = unit / a.h_kv;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int everyone = cs * kSelThreads, me = rank * kSelThreads + tid;
+  dev::launch_dependents();
+
+  if (blockIdx.x == 0) {   // the call's status: a length outside [0, n_k]?
+    bool bad = false;
+    for (int i = tid; i < a.batch; i += kSelThreads) dev::clamp_len(a.kv_len, i, a.n_k, &bad);
+    bad = __syncthreads_or(bad);
+    if (tid == 0) {
+      a.status[kStatusCode] = 0;
+      a.status[kStatusLen] = bad ? CRISP_ERR_INVALID_ARG : 0;
+    }
   }
+  const int len = dev::clamp_len(a.kv_len, b, a.n_k);
   int32_t* kept = a.kept + (int64_t)unit * a.budget;
   const int keep = min(len, a.budget);
-  if (tid == 0 && unit % a.h_kv == 0) a.new_len[b] = keep;
-  for (int i = keep + tid; i < a.budget; i += kSelThreads) kept[i] = -1;
+  if (me == 0 && unit == b * a.h_kv) a.new_len[b] = keep;
+  for (int i = keep + me; i < a.budget; i += everyone) kept[i] = -1;
   if (len <= a.budget) {
-    for (int i = tid; i < len; i += kSelThreads) kept[i] = i;
+    for (int i = me; i < len; i += everyone) kept[i] = i;
     return;
   }
   const float* score = a.score + (int64_t)unit * a.n_k;
-  const int m0 = a.sinks, m1 = len - a.recent;      // the keys that compete
+  const int m0 = a.sinks, m1 = len - a.recent;      // the keys between compete
+  for (int i = me; i < m0; i += everyone) kept[i] = i;
+  for (int i = me; i < a.recent; i += everyone) kept[a.budget - a.recent + i] = m1 + i;
   int want = a.budget - a.sinks - a.recent;         // < m1 - m0
-  // radix select: the want-th largest key, level by level
+  if (want == 0) return;
+
+  // this CTA's stretch
+  const int seg = ((m1 - m0 + cs - 1) / cs + 31) & ~31;
+  const int s0 = min(m1, m0 + rank * seg), n = min(m1, s0 + seg) - s0;
+  const bool hold = seg <= kCachedKeys;
+  for (int i = tid; i < 3 * kBins; i += kSelThreads) hist[i / kBins][i % kBins] = 0;
+  __syncthreads();
+  const float* mine = score + s0;
+  auto key_at = [&](int i) { return hold ? cached[i] : score_key(mine[i]); };
+
   uint32_t prefix = 0, mask = 0;
   const int shift[3] = {21, 10, 0}, bits[3] = {11, 11, 10};
-  if (want > 0) {
-    for (int lev = 0; lev < 3; ++lev) {
-      for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
-      const uint32_t bm = (1u << bits[lev]) - 1u;
-      for (int j = m0 + tid; j < m1; j += kSelThreads) {
-        const uint32_t key = score_key(score[j]);
-        if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift[lev]) & bm], 1);
+#pragma unroll
+  for (int lev = 0; lev < 3; ++lev) {
+    const uint32_t bm = (1u << bits[lev]) - 1u;
+    if (lev == 0) {
+      int i = tid;
+      for (; i + 3 * kSelThreads < n; i += 4 * kSelThreads) {
+        float x[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) x[q] = mine[i + q * kSelThreads];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t key = score_key(x[q]);
+          if (hold) cached[i + q * kSelThreads] = key;
+          atomicAdd(&hist[0][key >> shift[0]], 1);
+        }
       }
-      __syncthreads();
-      // bins from the top: thread t owns bins top - 2t and top - 2t - 1
-      const int top = kBins - 1 - 2 * tid;
-      const int c0 = hist[top], c1 = hist[top - 1];
-      int total;
-      const int above = cta_scan(c0 + c1, warp_sums, &total);
-      if (above < want && above + c0 >= want) {
-        found_bin = (uint32_t)top;
-        found_above = above;
-      } else if (above + c0 < want && above + c0 + c1 >= want) {
-        found_bin = (uint32_t)(top - 1);
-        found_above = above + c0;
+      for (; i < n; i += kSelThreads) {
+        const uint32_t key = score_key(mine[i]);
+        if (hold) cached[i] = key;
+        atomicAdd(&hist[0][key >> shift[0]], 1);
       }
-      __syncthreads();
-      prefix |= found_bin << shift[lev];
-      mask |= bm << shift[lev];
-      want -= found_above;
-      __syncthreads();
+    } else {
+      for (int i = tid; i < n; i += kSelThreads) {
+        const uint32_t key = key_at(i);
+        if ((key & mask) == prefix) atomicAdd(&hist[lev][(key >> shift[lev]) & bm], 1);
+      }
     }
+    if (cs > 1) cluster.sync(); else __syncthreads();
+    // bins from the top: thread t owns bins top = last - 2t and top - 1, summed over the cluster
+    const int top = kBins - 1 - 2 * tid;
+    int c0 = 0, c1 = 0;
+    for (int r = 0; r < cs; ++r) {
+      const int2 c = *reinterpret_cast<const int2*>((cs > 1 ? cluster.map_shared_rank(hist[lev], r) : hist[lev]) + top - 1);
+      c0 += c.y;
+      c1 += c.x;
+    }
+    const int above = cta_scan(c0 + c1, warp_sums);
+    if (above < want && above + c0 >= want) {
+      found_bin = (uint32_t)top;
+      found_above = above;
+    } else if (above + c0 < want && above + c0 + c1 >= want) {
+      found_bin = (uint32_t)(top - 1);
+      found_above = above + c0;
+    }
+    __syncthreads();
+    prefix |= found_bin << shift[lev];
+    mask |= bm << shift[lev];
+    want -= found_above;
+    __syncthreads();
   }
-  // keys above the cut stay, and the first `want` equal to it
+  // keys above the cut stay, and the first `want` equal to it. Each warp has
+  // a contiguous stretch: counts first, then positions.
   const uint32_t cut = prefix;
-  const bool any = a.budget > a.sinks + a.recent;
-  int done = 0, ties = 0;
-  for (int j0 = 0; j0 < len; j0 += kSelThreads) {
-    const int j = j0 + tid;
-    bool stay = false, tie = false;
-    if (j < len) {
-      if (j < m0 || j >= m1) {
-        stay = true;
-      } else if (any) {
-        const uint32_t key = score_key(score[j]);
-        stay = key > cut;
-        tie = key == cut;
-      }
-    }
-    int n_tie, n_stay;
-    const int t = ties + cta_scan(tie ? 1 : 0, warp_sums, &n_tie);
-    if (tie && t < want) stay = true;
-    const int at = done + cta_scan(stay ? 1 : 0, warp_sums, &n_stay);
-    if (stay) kept[at] = j;
-    ties += n_tie;
-    done += n_stay;
+  const int chunk = ((n + kSelWarps - 1) / kSelWarps + 31) & ~31;
+  const int w0 = min(n, warp * chunk), w1 = min(n, w0 + chunk);
+  int n_above = 0, n_ties = 0;
+  for (int i0 = w0; i0 < w1; i0 += 32) {
+    const bool in = i0 + lane < w1;
+    const uint32_t key = in ? key_at(i0 + lane) : 0u;
+    n_above += __popc(__ballot_sync(0xffffffffu, in && key > cut));
+    n_ties += __popc(__ballot_sync(0xffffffffu, in && key == cut));
   }
+  if (lane == 0) {
+    warp_above[warp] = n_above;
+    warp_ties[warp] = n_ties;
+  }
+  __syncthreads();
+  int before_above = 0, before_ties = 0;
+  if (warp == 0) {
+    int x = warp_above[lane], y = warp_ties[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int p = __shfl_up_sync(0xffffffffu, x, d), q = __shfl_up_sync(0xffffffffu, y, d);
+      if (lane >= d) x += p, y += q;
+    }
+    warp_above[lane] = x;   // inclusive
+    warp_ties[lane] = y;
+    if (lane == 31) {
+      cta_counts[0] = x;
+      cta_counts[1] = y;
+    }
+  }
+  if (cs > 1) cluster.sync(); else __syncthreads();
+  for (int r = 0; r < rank; ++r) {
+    const int* c = cluster.map_shared_rank(cta_counts, r);
+    before_above += c[0];
+    before_ties += c[1];
+  }
+  if (warp > 0) {
+    before_above += warp_above[warp - 1];
+    before_ties += warp_ties[warp - 1];
+  }
+  const uint32_t lower = (1u << lane) - 1u;
+  for (int i0 = w0; i0 < w1; i0 += 32) {
+    const bool in = i0 + lane < w1;
+    const uint32_t key = in ? key_at(i0 + lane) : 0u;
+    const bool up = in && key > cut, tie = in && key == cut;
+    const uint32_t ups = __ballot_sync(0xffffffffu, up), ties = __ballot_sync(0xffffffffu, tie);
+    const int t = before_ties + __popc(ties & lower);
+    if (up || (tie && t < want)) kept[m0 + before_above + __popc(ups & lower) + min(t, want)] = s0 + i0 + lane;
+    before_above += __popc(ups);
+    before_ties += __popc(ties);
+  }
+  if (cs > 1) cluster.sync();   // nobody leaves while its counts may be read
 }
 
-// One warp per kept key: its key row, value row and score; the scores behind
-// the last kept key become 0.
-__global__ void __launch_bounds__(256) evict_gather_kernel(EvictArgs a) {
+// Eight kept keys per warp: their key rows, value rows and scores; the scores
+// behind the last kept key become 0. All loads of a warp are in flight at
+// once. VEC: 16-byte pieces of a key's K and V rows per lane (1 bf16, 2 fp32).
+template <int VEC>
+__global__ void __launch_bounds__(256) evict_move_kernel(EvictArgs a) {
   const int unit = blockIdx.y, b = unit / a.h_kv, g = unit - b * a.h_kv;
   const int lane = threadIdx.x & 31;
-  const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (i >= a.n_new) return;
-  const int j = i < a.budget ? a.kept[(int64_t)unit * a.budget + i] : -1;
-  float* sn = a.score_new + (int64_t)unit * a.n_new + i;
-  if (j < 0) {
-    if (lane == 0) *sn = 0.f;
-    return;
+  const int i0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * kMoveKeys;
+  if (i0 >= a.n_new) return;
+  constexpr int es = VEC * 2;   // element size
+  constexpr int row16 = VEC * 16;   // 16-byte pieces per row
+  dev::wait_for_launches();
+  int j = -1;
+  float sc = 0.f;
+  if (lane < kMoveKeys && i0 + lane < a.budget) {
+    j = a.kept[(int64_t)unit * a.budget + i0 + lane];
+    if (j >= 0) sc = a.score[(int64_t)unit * a.n_k + j];
   }
-  const int es = a.row_bytes / kHeadDim;   // element size
-  auto row = [&](const void* p, const Strides& s, int64_t t) {
-    return static_cast<const char*>(p) + (b * s.seq + g * s.head + t * s.token) * es;
-  };
-  const char* ks = row(a.k, a.sk, j);
-  const char* vs = row(a.v, a.sv, j);
-  char* kd = const_cast<char*>(row(a.k_new, a.skn, i));
-  char* vd = const_cast<char*>(row(a.v_new, a.svn, i));
-  for (int o = lane * 16; o < 2 * a.row_bytes; o += 512) {
-    if (o < a.row_bytes)
-      *reinterpret_cast<uint4*>(kd + o) = *reinterpret_cast<const uint4*>(ks + o);
-    else
-      *reinterpret_cast<uint4*>(vd + o - a.row_bytes) = *reinterpret_cast<const uint4*>(vs + o - a.row_bytes);
+  const char* k0 = static_cast<const char*>(a.k) + (b * a.sk.seq + g * a.sk.head) * es;
+  const char* v0 = static_cast<const char*>(a.v) + (b * a.sv.seq + g * a.sv.head) * es;
+  char* kn = static_cast<char*>(a.k_new) + (b * a.skn.seq + g * a.skn.head) * es;
+  char* vn = static_cast<char*>(a.v_new) + (b * a.svn.seq + g * a.svn.head) * es;
+  uint4 x[kMoveKeys][VEC];
+  int from[kMoveKeys];
+#pragma unroll
+  for (int q = 0; q < kMoveKeys; ++q) {
+    from[q] = __shfl_sync(0xffffffffu, j, q);
+    if (from[q] >= 0) {
+#pragma unroll
+      for (int p = 0; p < VEC; ++p) {
+        const int c = p * 32 + lane;
+        const char* src = c < row16 ? k0 + (int64_t)from[q] * a.sk.token * es + c * 16
+                                    : v0 + (int64_t)from[q] * a.sv.token * es + (c - row16) * 16;
+        x[q][p] = __ldcs(reinterpret_cast<const uint4*>(src));
+      }
+    }
   }
-  if (lane == 0) *sn = a.score[(int64_t)unit * a.n_k + j];
+#pragma unroll
+  for (int q = 0; q < kMoveKeys; ++q) {
+    if (from[q] >= 0) {
+#pragma unroll
+      for (int p = 0; p < VEC; ++p) {
+        const int c = p * 32 + lane;
+        char* dst = c < row16 ? kn + (int64_t)(i0 + q) * a.skn.token * es + c * 16
+                              : vn + (int64_t)(i0 + q) * a.svn.token * es + (c - row16) * 16;
+        *reinterpret_cast<uint4*>(dst) = x[q][p];
+      }
+    }
+  }
+  if (lane < kMoveKeys && i0 + lane < a.n_new) a.score_new[(int64_t)unit * a.n_new + i0 + lane] = sc;
 }
 
 }  // namespace
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st) {
   const int units = a.batch * a.h_kv;
-  evict_select_kernel<<<units, kSelThreads, 0, st>>>(a);
-  cudaError_t e = cudaGetLastError();
+  // a cluster per head: about 8192 keys per CTA, while that does not ask for more than two CTAs per SM
+  int cs = 1;
+  while (cs < 8 && (int64_t)cs * 8192 < a.n_k && 2 * cs * units <= 296) cs *= 2;
+  while (cs < 8 && (int64_t)cs * kCachedKeys < a.n_k) cs *= 2;   // or the keys would be read from memory four times
+  const int64_t stretch = ((a.n_k + cs - 1) / cs + 31) / 32 * 32;
+  const size_t smem = 4 * (size_t)(stretch < kCachedKeys ? stretch : kCachedKeys);
+  cudaError_t e =
+      cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kCachedKeys);
   if (e != cudaSuccess) return e;
-  evict_gather_kernel<<<dim3((a.n_new + 7) / 8, units), 256, 0, st>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(units * cs));
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = cs;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a, cs)) != cudaSuccess) return e;
+  cfg.gridDim = dim3((a.n_new + 8 * kMoveKeys - 1) / (8 * kMoveKeys), units);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  return a.row_bytes == 2 * kHeadDim ? cudaLaunchKernelEx(&cfg, evict_move_kernel<1>, a)
+                                     : cudaLaunchKernelEx(&cfg, evict_move_kernel<2>, a);
 }
 
 }  // namespace crisp
