@@ -419,18 +419,15 @@ class CacheConfig:
         self.__dict__["_kept"] = None
 
     def _c(self, **tensors) -> _CacheCfg:
-        """The C structure for these tensors' strides (the last one when nothing has changed)."""
-        strides = tuple(t.stride() for t in tensors.values())
-        kept = self._kept
-        if kept is not None and kept[0] == strides and kept[1] == tuple(tensors):
-            return kept[2]
+        """A C structure for these tensors' strides."""
         c = _CacheCfg()
         for f in _CACHE_INTS + ["sm_scale", "reserved"]:
             setattr(c, f, getattr(self, f))
         if self.workspace is not None:
             c.workspace = self.workspace.data_ptr()
             c.workspace_bytes = self.workspace.numel() * self.workspace.element_size()
-        for (f, t), st in zip(tensors.items(), strides):
+        for f, t in tensors.items():
+            st = t.stride()
             if st[-1] != 1 and t.shape[-1] != 1:
                 raise ValueError(f"{f}: the head dimension has to be contiguous")
             if any(s <= 0 for s, n in zip(st, t.shape) if n > 1):
@@ -439,8 +436,17 @@ class CacheConfig:
             if seq == head == token == 0:
                 token = self.d
             setattr(c, f, _Strides(seq, head, token))
-        self.__dict__["_kept"] = (strides, tuple(tensors), c)
         return c
+
+    def _ref(self, names, tensors):
+        """A reference to the C structure for these tensors; the last one is kept while nothing changes."""
+        strides = [t.stride() for t in tensors]
+        kept = self._kept
+        if kept is not None and kept[0] == strides and kept[1] is names:
+            return kept[2]
+        c = self._c(**dict(zip(names, tensors)))
+        self.__dict__["_kept"] = (strides, names, ctypes.byref(c))
+        return self._kept[2]
 
     def allocate_workspace(self, op: int, device="cuda"):
         """Device workspace for operator `op` (CACHE_WINDOW, CACHE_SCORED, CACHE_PREFIX, CACHE_EVICT); the
@@ -457,87 +463,90 @@ def cache_workspace_size(cfg: CacheConfig, op: int) -> int:
     return out.value
 
 
-def _cache_device(first, dtype, tensors, words):
-    """Checks types, shapes and devices; returns the tensors' device. `tensors` are (name, tensor, shape) of the
-    layer's type, `words` (name, tensor or None, shape, type name) of 4-byte types, contiguous."""
+_ATTEND, _SHARED = ("q", "k", "v", "out"), ("q", "k_prefix", "v_prefix", "k", "v", "out")
+_EVICT = ("k", "v", "k_new", "v_new")
+
+
+def _expect(name, t, dtype, shape, dev):
+    raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _cache_call(fn, cfg, stream, names, tensors, shapes, words, args):
+    """Checks the tensors (of the layer's type, with their shapes) and the words (name, tensor or None, type, shape;
+    contiguous), and calls the library's `fn` with the tensors' device current, on `stream` (default: that device's
+    current stream)."""
     import torch
-    dev = first.device
+    dev = tensors[0].device
     if dev.type != "cuda":
         raise ValueError("the cache operators take CUDA tensors")
-    want = torch.float32 if dtype == FP32 else torch.bfloat16
-    for name, t, shape in tensors:
-        if t.dtype != want or t.device != dev or t.shape != shape:
-            raise ValueError(f"{name}: expected {want} {tuple(shape)} on {dev}, got {t.dtype} {tuple(t.shape)} on "
-                             f"{t.device}")
-    for name, t, shape, kind in words:
-        if t is None:
-            continue
-        if t.dtype != getattr(torch, kind) or t.device != dev or t.shape != shape or not t.is_contiguous():
-            raise ValueError(f"{name}: expected contiguous torch.{kind} {tuple(shape)} on {dev}, got {t.dtype} "
-                             f"{tuple(t.shape)} on {t.device}")
-    return dev
-
-
-def _on_device(dev, cfg, stream, name, *args):
-    """Calls the library with `dev` current, on `stream` (default: that device's current stream)."""
-    import torch
+    want = torch.float32 if cfg.dtype == FP32 else torch.bfloat16
+    for name, t, shape in zip(names, tensors, shapes):
+        if t.dtype is not want or t.shape != shape or t.device != dev:
+            _expect(name, t, want, shape, dev)
+    for name, t, kind, shape in words:
+        if t is not None and (t.dtype is not kind or t.shape != shape or t.device != dev or not t.is_contiguous()):
+            _expect(name, t, f"contiguous {kind}", shape, dev)
     if cfg.workspace is not None and cfg.workspace.device != dev:
         raise ValueError(f"the workspace is on {cfg.workspace.device}, the tensors are on {dev}")
-    fn = getattr(lib(), name)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    raw = getattr(stream, "cuda_stream", stream)
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, raw), name)
+    ref = cfg._ref(names, tensors)
+    # torch.cuda.current_stream(dev).cuda_stream without the stream object (3 us of a small call's 15)
+    raw = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else getattr(stream, "cuda_stream", stream)
+    if dev.index == torch._C._cuda_getDevice():
+        code = fn(*args, ref, raw)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, raw), name)
+            code = fn(*args, ref, raw)
+    if code != 0:
+        raise CrispError(code, fn.__name__)
 
 
 def window_attention(q, k, v, out, cfg: CacheConfig, kv_len=None, stream=None) -> None:
     """crisp_window_attention: the newest n_q tokens of every sequence attend through a window of cfg.window keys
     (0: all) and the first cfg.sinks keys."""
-    qs, ks = (cfg.batch, cfg.h_q, cfg.n_q, cfg.d), (cfg.batch, cfg.h_kv, cfg.n_k, cfg.d)
-    dev = _cache_device(q, cfg.dtype, (("q", q, qs), ("k", k, ks), ("v", v, ks), ("out", out, qs)),
-                        (("kv_len", kv_len, (cfg.batch,), "int32"),))
-    _on_device(dev, cfg, stream, "crisp_window_attention", q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-               _ptr(kv_len), ctypes.byref(cfg._c(q=q, k=k, v=v, out=out)))
+    import torch
+    b = cfg.batch
+    qs, ks = (b, cfg.h_q, cfg.n_q, cfg.d), (b, cfg.h_kv, cfg.n_k, cfg.d)
+    _cache_call(lib().crisp_window_attention, cfg, stream, _ATTEND, (q, k, v, out), (qs, ks, ks, qs),
+                (("kv_len", kv_len, torch.int32, (b,)),),
+                (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(kv_len)))
 
 
 def scored_attention(q, k, v, out, score, cfg: CacheConfig, kv_len=None, stream=None) -> None:
     """crisp_scored_attention: window_attention for n_q <= 16 that adds every key's softmax weights to
     score (float32 [batch, h_kv, n_k])."""
-    qs, ks = (cfg.batch, cfg.h_q, cfg.n_q, cfg.d), (cfg.batch, cfg.h_kv, cfg.n_k, cfg.d)
-    dev = _cache_device(q, cfg.dtype, (("q", q, qs), ("k", k, ks), ("v", v, ks), ("out", out, qs)),
-                        (("kv_len", kv_len, (cfg.batch,), "int32"), ("score", score, ks[:3], "float32")))
-    _on_device(dev, cfg, stream, "crisp_scored_attention", q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-               _ptr(score), _ptr(kv_len), ctypes.byref(cfg._c(q=q, k=k, v=v, out=out)))
+    import torch
+    b = cfg.batch
+    qs, ks = (b, cfg.h_q, cfg.n_q, cfg.d), (b, cfg.h_kv, cfg.n_k, cfg.d)
+    _cache_call(lib().crisp_scored_attention, cfg, stream, _ATTEND, (q, k, v, out), (qs, ks, ks, qs),
+                (("kv_len", kv_len, torch.int32, (b,)), ("score", score, torch.float32, ks[:3])),
+                (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(score), _ptr(kv_len)))
 
 
 def shared_prefix_attention(q, k_prefix, v_prefix, k, v, out, cfg: CacheConfig, kv_len=None, stream=None) -> None:
     """crisp_shared_prefix_attention: every sequence attends over the shared k_prefix, v_prefix
     [h_kv, n_prefix, d] and its own keys."""
-    qs, ks = (cfg.batch, cfg.h_q, cfg.n_q, cfg.d), (cfg.batch, cfg.h_kv, cfg.n_k, cfg.d)
+    import torch
+    b = cfg.batch
+    qs, ks = (b, cfg.h_q, cfg.n_q, cfg.d), (b, cfg.h_kv, cfg.n_k, cfg.d)
     ps = (cfg.h_kv, cfg.n_prefix, cfg.d)
-    dev = _cache_device(q, cfg.dtype, (("q", q, qs), ("k_prefix", k_prefix, ps), ("v_prefix", v_prefix, ps),
-                                       ("k", k, ks), ("v", v, ks), ("out", out, qs)),
-                        (("kv_len", kv_len, (cfg.batch,), "int32"),))
-    _on_device(dev, cfg, stream, "crisp_shared_prefix_attention", q.data_ptr(), k_prefix.data_ptr(),
-               v_prefix.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(kv_len),
-               ctypes.byref(cfg._c(q=q, k_prefix=k_prefix, v_prefix=v_prefix, k=k, v=v, out=out)))
+    _cache_call(lib().crisp_shared_prefix_attention, cfg, stream, _SHARED, (q, k_prefix, v_prefix, k, v, out),
+                (qs, ps, ps, ks, ks, qs), (("kv_len", kv_len, torch.int32, (b,)),),
+                (q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                 _ptr(kv_len)))
 
 
 def evict(k, v, score, k_new, v_new, score_new, kept, new_len, cfg: CacheConfig, kv_len=None, stream=None) -> None:
     """crisp_evict: the first cfg.sinks, the last cfg.recent and the highest scored keys, cfg.budget in all, move to
     the new cache; kept (int32 [batch, h_kv, budget]) gets their old indices, new_len (int32 [batch]) the lengths."""
-    ks, ns = (cfg.batch, cfg.h_kv, cfg.n_k, cfg.d), (cfg.batch, cfg.h_kv, cfg.n_new, cfg.d)
-    dev = _cache_device(k, cfg.dtype, (("k", k, ks), ("v", v, ks), ("k_new", k_new, ns), ("v_new", v_new, ns)),
-                        (("kv_len", kv_len, (cfg.batch,), "int32"), ("score", score, ks[:3], "float32"),
-                         ("score_new", score_new, ns[:3], "float32"),
-                         ("kept", kept, (*ks[:2], cfg.budget), "int32"), ("new_len", new_len, (cfg.batch,), "int32")))
-    _on_device(dev, cfg, stream, "crisp_evict", k.data_ptr(), v.data_ptr(), _ptr(score), _ptr(kv_len),
-               k_new.data_ptr(), v_new.data_ptr(), _ptr(score_new), _ptr(kept), _ptr(new_len),
-               ctypes.byref(cfg._c(k=k, v=v, k_new=k_new, v_new=v_new)))
+    import torch
+    b = cfg.batch
+    ks, ns = (b, cfg.h_kv, cfg.n_k, cfg.d), (b, cfg.h_kv, cfg.n_new, cfg.d)
+    i32, f32 = torch.int32, torch.float32
+    _cache_call(lib().crisp_evict, cfg, stream, _EVICT, (k, v, k_new, v_new), (ks, ks, ns, ns),
+                (("kv_len", kv_len, i32, (b,)), ("score", score, f32, ks[:3]), ("score_new", score_new, f32, ns[:3]),
+                 ("kept", kept, i32, (b, cfg.h_kv, cfg.budget)), ("new_len", new_len, i32, (b,))),
+                (k.data_ptr(), v.data_ptr(), _ptr(score), _ptr(kv_len), k_new.data_ptr(), v_new.data_ptr(),
+                 _ptr(score_new), _ptr(kept), _ptr(new_len)))
 
 
 def cache_device_status(cfg: CacheConfig, stream=None) -> int:

@@ -56,7 +56,8 @@ enum {
   B_SFULL = B_VCLEAR + kVStages,   // [2]: S_X landed
   B_PFULL = B_SFULL + 2,           // [2]: P_X written (128 arrivals)
   B_DONE = B_PFULL + 2,            // [2]: last P_X V landed
-  B_DRAIN = B_DONE + 2,
+  B_Q = B_DONE + 2,                // [2]: Q_X staged (128 arrivals)
+  B_DRAIN = B_Q + 2,
   B_COUNT = B_DRAIN + 1
 };
 constexpr uint32_t OFF_TMEMPTR = OFF_BAR + 8 * B_COUNT;
@@ -168,26 +169,11 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       dev::mbar_init(bar_addr(sbase, B_SFULL + x), 1);
       dev::mbar_init(bar_addr(sbase, B_PFULL + x), 128);
       dev::mbar_init(bar_addr(sbase, B_DONE + x), 1);
+      dev::mbar_init(bar_addr(sbase, B_Q + x), 128);
     }
     dev::mbar_init(bar_addr(sbase, B_DRAIN), 1);
     dev::fence_mbar_init();
   }
-  // queries: 16-byte pieces into the 128-byte swizzled layout; rows past the unit's end are zero
-  for (int e = threadIdx.x; e < 256 * 16; e += kThreads) {
-    const int r = e >> 4, c = e & 15;
-    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    if (r0 + r < a.rows) {
-      const dev::Row w = dev::unit_row(a, b, g, r0 + r);
-      x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + w.b * a.sq.seq + w.h * a.sq.head +
-                                          w.i * a.sq.token + c * 8);
-    }
-    const uint32_t off = OFF_Q + (r >> 7) * kTileBytes + (c >> 3) * kHalfBytes + (r & 127) * 128 +
-                         (((c & 7) ^ (r & 7)) << 4);
-    *reinterpret_cast<uint4*>(sgen + off) = x;
-  }
-  dev::fence_proxy_async_smem();
-  __syncthreads();
-  if (*abort_flag) return;   // uniform: read after the barrier, before any TMEM is taken
   if (warp == 1) {
     dev::tmem_alloc(dev::smem_u32(tmem_ptr_smem), kTmemCols);
     dev::tmem_relinquish();
@@ -196,6 +182,10 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   __syncthreads();
   dev::tc_fence_after();
   const uint32_t tmem = *tmem_ptr_smem;
+  if (*abort_flag) {   // uniform: written before the barrier; later failures are met in the waits
+    if (warp == 1) dev::tmem_dealloc(tmem, kTmemCols);
+    return;
+  }
 
   if (warp < 4) dev::regs_release<kRegsControl>();
   if (warp == 0) {
@@ -292,8 +282,9 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       return true;
     };
     int t = sc.t0, ka = 0, kb = 0;
-    bool ok = true;
-    bool have = sc.next(t, ka, kb);
+    bool ok = warp_wait(bar_addr(sbase, B_Q), 0, abort_flag, a.status, 14) &&
+              (!hasB || warp_wait(bar_addr(sbase, B_Q + 1), 0, abort_flag, a.status, 15));
+    bool have = ok && sc.next(t, ka, kb);
     if (have) {
       ok = warp_wait(bar_addr(sbase, B_KFULL + 0), 0, abort_flag, a.status, 6);
       dev::tc_fence_after();
@@ -357,6 +348,30 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       const bool in = row < a.rows;
       const dev::Row w = dev::unit_row(a, b, g, in ? row : 0);
       const int pos = in ? dev::row_pos(a, len, w.i) : -1;
+      {
+        // the tile's queries into the 128-byte swizzled layout, half a warp
+        // per row, all loads in flight at once; rows past the unit's end are zero
+        const int c = lane & 15;
+        uint4 qv[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int qr = r0 + x * 128 + quarter * 32 + e * 2 + (lane >> 4);
+          qv[e] = make_uint4(0u, 0u, 0u, 0u);
+          if (qr < a.rows) {
+            const dev::Row y = dev::unit_row(a, b, g, qr);
+            qv[e] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + y.b * a.sq.seq +
+                                                    y.h * a.sq.head + y.i * a.sq.token + c * 8);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int qr = quarter * 32 + e * 2 + (lane >> 4);
+          *reinterpret_cast<uint4*>(sgen + OFF_Q + x * kTileBytes + (c >> 3) * kHalfBytes + qr * 128 +
+                                    (((c & 7) ^ (qr & 7)) << 4)) = qv[e];
+        }
+        dev::fence_proxy_async_smem();
+        dev::mbar_arrive(bar_addr(sbase, B_Q + x));
+      }
       const float sl2 = a.scale_log2;
       float m_ref = -INFINITY, l = 0.f;
       int k = 0;

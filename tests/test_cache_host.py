@@ -78,9 +78,13 @@ def test_cfg_init_matches_python_config():
 
 def test_changed_config_makes_a_new_struct():
     cfg = crisp.CacheConfig(batch=1, n_q=1, n_k=64, h_q=8, h_kv=8)
-    assert cfg._c() is cfg._c()
+    torch = pytest.importorskip("torch")
+    names, t = ("k",), [torch.zeros(1, 8, 64, 128)]
+    ref = cfg._ref(names, t)
+    assert cfg._ref(names, t) is ref
     cfg.window = 7
-    assert cfg._c().window == 7
+    assert cfg._ref(names, t)._obj.window == 7
+    assert cfg._ref(names, [torch.zeros(1, 64, 8, 128).transpose(1, 2)])._obj.k.head == 128
 
 
 @pytest.mark.parametrize("op", OPS)
