@@ -78,7 +78,8 @@ struct RowMap {
 // consecutive slots of `block` rows each. kSplits: slot = job * splits + s.
 // kStair: the launch's key tiles are dealt to `ctas` CTAs as equal runs of one
 // flat list; slot = CTA + job (unique: both only grow along the list).
-enum PartMode : int { kPartNone = 0, kSplits = 1, kStair = 2 };
+// kBoxes: the tcgen05 kernel's row tiles, two per job; slot = job * splits + s.
+enum PartMode : int { kPartNone = 0, kSplits = 1, kStair = 2, kBoxes = 3 };
 struct PartSrc {
   int mode;
   const float* o;       // [slot][block][128], not normalised
@@ -87,7 +88,11 @@ struct PartSrc {
   int blocks;           // row blocks per unit
   int splits;
   const int2* table;    // kStair: [job] first and last CTA
+  int tok_box, seq_box; // kBoxes
 };
+
+// x / d as (x * div_magic(d)) >> 36, exact while x * d < 2^36 (rows < 2^28, d <= 256).
+inline uint64_t div_magic(int d) { return (((uint64_t)1 << 36) + d - 1) / d; }
 
 // Arguments shared by the attention kernels.
 struct CacheArgs {
@@ -101,6 +106,10 @@ struct CacheArgs {
   int rows, per_seq;       // rows per unit; rows per sequence within it
   int sets_status;         // the call's only kernel that reports: it sets the status words instead of a memset
   int prefix;              // rows run over every sequence, every key is seen
+  int tok_box, seq_box;    // tcgen05 kernel: tokens and sequences of a row tile
+  int row_tiles;           // per unit
+  int n_seqs;              // sequences of q
+  uint64_t group_mul, seq_mul;   // div_magic(group), div_magic(per_seq)
   float scale_log2;
   Strides sq, sk, sv, so;
   // partial results (NULL: write the output rows)
@@ -146,10 +155,10 @@ __device__ __forceinline__ Row unit_row(const CacheArgs& a, int b, int g, int r)
   Row x;
   x.b = b;
   if (a.prefix) {
-    x.b = r / a.per_seq;
+    x.b = (int)(((uint64_t)r * a.seq_mul) >> 36);
     r -= x.b * a.per_seq;
   }
-  x.i = r / a.group;
+  x.i = (int)(((uint64_t)r * a.group_mul) >> 36);
   x.h = g * a.group + (r - x.i * a.group);
   return x;
 }
@@ -235,6 +244,7 @@ __device__ __forceinline__ int stair_find(const int* cum, int batch, int x) {
 struct AttnPlan {
   int kernel;        // AttnKernel
   int block, blocks, splits, ctas, tile;
+  int tok_box, seq_box, row_tiles;   // kTileTc
   int units;
   size_t slots;      // partial slots (0: the kernel writes the output itself)
 };

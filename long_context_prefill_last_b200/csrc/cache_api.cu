@@ -137,15 +137,20 @@ AttnPlan plan_tile(int units, int rows, int keys) {
   return p;
 }
 
-// Grid of the tcgen05 kernel: one CTA per SM; key lists are split while that
-// fills more SMs, with at least two key tiles in each split.
-AttnPlan plan_tc(int units, int rows, int keys) {
+// Grid of the tcgen05 kernel: one CTA per SM and pair of row tiles; key lists
+// are split while that fills more SMs, with at least two key tiles in each
+// split. A row tile holds up to 128 rows: the group's heads of as many tokens
+// as fit (of as many sequences as fit, for the prefix).
+AttnPlan plan_tc(int units, int group, int n_q, int seqs, bool prefix, int keys) {
   AttnPlan p{};
   p.kernel = kTileTc;
   p.units = units;
   p.tile = 128;
   p.block = 256;
-  p.blocks = (rows + 255) / 256;
+  p.tok_box = std::min(n_q, 128 / group);
+  p.seq_box = prefix && p.tok_box == n_q ? std::min(seqs, 128 / (group * n_q)) : 1;
+  p.row_tiles = (n_q + p.tok_box - 1) / p.tok_box * (prefix ? (seqs + p.seq_box - 1) / p.seq_box : 1);
+  p.blocks = (p.row_tiles + 1) / 2;
   const int64_t jobs = (int64_t)units * p.blocks;
   const int tiles = (keys + 127) / 128;
   p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(kSms / jobs, tiles / 2));
@@ -192,12 +197,13 @@ CachePlan plan_cache(const CacheShape& s, int op) {
     p.has_pre = op == CRISP_CACHE_PREFIX;
     // fp32: the CUDA-core tiles; bf16: drafts, and a prefix that at most 64 rows
     // read, take the decode kernel, more rows the tcgen05 tiles
-    auto plan = [&](int n_units, int n_rows, int n_keys, bool few) {
+    auto plan = [&](int n_units, int n_rows, int n_keys, bool few, bool prefix) {
       return s.fp32 ? plan_tile(n_units, n_rows, n_keys)
-                    : few ? plan_decode(n_units, n_rows, n_keys) : plan_tc(n_units, n_rows, n_keys);
+             : few  ? plan_decode(n_units, n_rows, n_keys)
+                    : plan_tc(n_units, s.group, s.n_q, s.batch, prefix, n_keys);
     };
-    p.main = plan(units, rows, keys, s.n_q <= kMaxDraft);
-    if (p.has_pre) p.pre = plan(s.h_kv, s.batch * rows, s.n_prefix, s.batch * rows <= 64);
+    p.main = plan(units, rows, keys, s.n_q <= kMaxDraft, false);
+    if (p.has_pre) p.pre = plan(s.h_kv, s.batch * rows, s.n_prefix, s.batch * rows <= 64, true);
     // output rows straight away when no row's keys are split
     if (op == CRISP_CACHE_WINDOW && p.main.kernel != kDecodeMma && p.main.splits == 1) p.main.slots = 0;
     // a row's pieces are read by one warp while there are few, by up to eight when there are many
@@ -247,6 +253,9 @@ crisp_status run_attention(const void* q, const void* kp, const void* vp, const 
   a.group = s.group;
   a.n_q = s.n_q;
   a.per_seq = s.n_q * s.group;
+  a.n_seqs = s.batch;
+  a.group_mul = div_magic(a.group);
+  a.seq_mul = div_magic(a.per_seq);
   a.scale_log2 = s.scale_log2;
   a.sq = s.q;
   a.so = s.out;
@@ -257,10 +266,15 @@ crisp_status run_attention(const void* q, const void* kp, const void* vp, const 
     x->blocks = pl.blocks;
     x->splits = pl.splits;
     x->ctas = pl.ctas;
+    x->tok_box = pl.tok_box;
+    x->seq_box = pl.seq_box;
+    x->row_tiles = pl.row_tiles;
     if (pl.slots == 0) return src;
     x->part_ml = reinterpret_cast<float2*>(ws + off_ml);
     x->part_o = reinterpret_cast<float*>(ws + off_o);
-    src.mode = pl.kernel == kDecodeMma ? kStair : kSplits;
+    src.mode = pl.kernel == kDecodeMma ? kStair : pl.kernel == kTileTc ? kBoxes : kSplits;
+    src.tok_box = pl.tok_box;
+    src.seq_box = pl.seq_box;
     src.o = x->part_o;
     src.ml = x->part_ml;
     src.block = pl.block;

@@ -36,7 +36,21 @@ __device__ __forceinline__ Pieces find_pieces(const FinishArgs& a, int b, int g,
     if (s.mode == kPartNone) continue;
     const int unit = src == 0 ? b * a.h_kv + g : g;
     const int r = src == 0 ? i * a.group + j : (b * a.n_q + i) * a.group + j;
-    const int blk = r / s.block, in = r - blk * s.block;
+    int blk, in;
+    if (s.mode == kBoxes) {
+      const int it = i / s.tok_box;
+      int ti = it, row = (i - it * s.tok_box) * a.group + j;
+      if (src == 1) {
+        const int bt = b / s.seq_box;
+        ti += bt * ((a.n_q + s.tok_box - 1) / s.tok_box);
+        row += (b - bt * s.seq_box) * s.tok_box * a.group;
+      }
+      blk = ti >> 1;
+      in = (ti & 1) * 128 + row;
+    } else {
+      blk = r / s.block;
+      in = r - blk * s.block;
+    }
     const int job = unit * s.blocks + blk;
     int64_t first = (int64_t)job * s.splits;
     int count = s.splits;

@@ -6,15 +6,21 @@
 //     o_r = sum_j 2^(x_rj - m_r) v_j / l_r,   x_rj = scale * log2(e) * q_r . k_j
 //
 // Bound: the tensor pipe (4 * 128 FLOP per row and key) beside the softmax's
-// issue slots. One CTA takes 256 rows of a unit (tiles A and B of 128) and a
-// range of its key tiles. A row is a (token, head of the group) pair, so the
-// query heads that share a key/value head read its tiles once, and the keys
-// that 256 rows span beyond the window are few (64 tokens at 4 heads a group).
-// Key tiles start at the first key that the CTA's rows see, wherever that is:
-// TMA boxes need no alignment along the tokens.
+// issue slots. One CTA takes two row tiles of a unit (A and B, up to 128 rows
+// each) and a range of its key tiles. A row tile is a TMA box of the query
+// tensor: the group's heads x a run of tokens (x sequences, for the prefix),
+// so the query heads that share a key/value head read its tiles once, and the
+// keys that a CTA's rows span beyond the window are few (64 tokens at 4 heads
+// a group). The same box of the output tensor takes the result. Key tiles
+// start at the first key that the CTA's rows see, wherever that is: TMA boxes
+// need no alignment along the tokens.
+//
+// A tile of at most 32 keys (a few first keys, a window's last ones) is
+// narrow: 32 columns of S, two K = 16 steps of P V, and a softmax over 32
+// columns.
 //
 // Warps, TMEM columns, register split and MMA order follow attn_tc.cu:
-//   warp 0       TMA producer: K (3-stage ring), V (2-stage ring); clears the
+//   warp 0       TMA producer: Q_A, Q_B, then K (3-stage ring), V (2-stage ring); clears the
 //                V rows behind the last key of a list segment, whose weights
 //                are zero but whose content may be anything
 //   warp 1       TMEM allocation; one elected lane issues every tcgen05.mma
@@ -56,7 +62,7 @@ enum {
   B_SFULL = B_VCLEAR + kVStages,   // [2]: S_X landed
   B_PFULL = B_SFULL + 2,           // [2]: P_X written (128 arrivals)
   B_DONE = B_PFULL + 2,            // [2]: last P_X V landed
-  B_Q = B_DONE + 2,                // [2]: Q_X staged (128 arrivals)
+  B_Q = B_DONE + 2,                // [2]: Q_X landed
   B_DRAIN = B_Q + 2,
   B_COUNT = B_DRAIN + 1
 };
@@ -66,6 +72,7 @@ constexpr uint32_t kSmemBytes = OFF_ABORT + 4 + 1024;   // + slack to align the 
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.f;
+constexpr int kNarrow = 32;
 
 __device__ __forceinline__ uint32_t bar_addr(uint32_t base, int i) { return base + OFF_BAR + 8u * i; }
 
@@ -75,12 +82,124 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return __all_sync(0xffffffffu, ok);
 }
 
-// 4-D tiled load (d, token, head, sequence); x is a multiple of 64 elements.
+// 4-D tiled load; x is a multiple of 64 elements.
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint32_t bar, int x, int y, int z, int w) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
       ::"r"(dst), "l"(tmap), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
       : "memory");
+}
+
+// 4-D tiled store; x is a multiple of 64 elements, no coordinate is negative.
+__device__ __forceinline__ void tma_store_4d(uint32_t src, const void* tmap, int x, int y, int z, int w) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];"
+               ::"l"(tmap), "r"(src), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+
+// Two K = 16 steps of D (+)= A * B, A in tensor memory (8 columns a step), B
+// MN-major, 128-byte swizzled in shared memory (128 in the start-address field a step).
+__device__ __forceinline__ void umma_ts2_w(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred e, p0, pt;\n\t.reg .b32 r, t;\n\t.reg .b64 b;\n\t"
+      "elect.sync r|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p0, %4, 0;\n\t"
+      "setp.eq.b32 pt, %4, %4;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p0;\n\t"
+      "add.u32 t, %1, 8;\n\tadd.s64 b, %2, 128;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [t], b, %3, pt;\n\t"
+      "}"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Bits lo .. hi - 1 of a 32-bit word (bounds may lie outside it).
+__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
+  const uint32_t below = hi >= 32 ? 0xffffffffu : hi <= 0 ? 0u : (1u << hi) - 1u;
+  const uint32_t skip = lo >= 32 ? 0xffffffffu : lo <= 0 ? 0u : (1u << lo) - 1u;
+  return below & ~skip;
+}
+
+// Per-row softmax state of a warp's 32 rows (one per lane).
+struct SoftRow {
+  float m_ref, l;
+};
+
+// One key tile of NC columns: logits from TMEM, unseen ones masked, running
+// statistics, weights back to TMEM as bf16. Column c is key k0 + c: seen for
+// low < c <= high or c < front, c <= high, when `part`.
+template <int NC>
+__device__ __forceinline__ void soft_tile(SoftRow& st, uint32_t s_col, uint32_t o_col, bool first, bool part, int low,
+                                          int high, int front, float sl2, uint32_t p_bar) {
+  float s[NC];
+#pragma unroll
+  for (int c0 = 0; c0 < NC; c0 += 32) dev::tmem_ld32(s_col + c0, reinterpret_cast<uint32_t(&)[32]>(s[c0]));
+  dev::tmem_wait_ld();
+  if (part) {
+#pragma unroll
+    for (int c0 = 0; c0 < NC; c0 += 32) {
+      const uint32_t seen = (bit_range(low + 1 - c0, 32) | bit_range(0, front - c0)) & bit_range(0, high + 1 - c0);
+#pragma unroll
+      for (int c = 0; c < 32; ++c) s[c0 + c] = (seen & (1u << c)) != 0u ? s[c0 + c] : -INFINITY;
+    }
+  }
+  float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+  for (int c = 4; c < NC - 4; c += 8) {
+    mx[0] = dev::max3(mx[0], s[c], s[c + 1]);
+    mx[1] = dev::max3(mx[1], s[c + 2], s[c + 3]);
+    mx[2] = dev::max3(mx[2], s[c + 4], s[c + 5]);
+    mx[3] = dev::max3(mx[3], s[c + 6], s[c + 7]);
+  }
+  mx[0] = dev::max3(mx[0], s[NC - 4], s[NC - 3]);
+  mx[1] = dev::max3(mx[1], s[NC - 2], s[NC - 1]);
+  const float tmax = fmaxf(dev::max3(mx[0], mx[1], mx[2]), mx[3]) * sl2;
+  const bool need = tmax > st.m_ref + kRescaleLog2 || (st.m_ref == -INFINITY && tmax > -INFINITY);
+  const float factor = need ? dev::ex2(st.m_ref - tmax) : 1.f;   // 0 when m_ref = -inf
+  if (!first && __any_sync(0xffffffffu, need)) {
+    // O holds P V of every earlier tile (it completed before S landed)
+#pragma unroll 1
+    for (int c0 = 0; c0 < 128; c0 += 32) {
+      uint32_t v[32];
+      dev::tmem_ld32(o_col + c0, v);
+      dev::tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * factor);
+      dev::tmem_st32(o_col + c0, v);
+    }
+  }
+  if (need) {
+    st.l *= factor;
+    st.m_ref = tmax;
+  }
+  const float neg_m = st.m_ref == -INFINITY ? 0.f : -st.m_ref;
+  // P = 2^(x - m), rounded to bf16 for the product with V (l keeps it in
+  // fp32); chunk c0 goes to S columns [c0/2, c0/2 + 16), already consumed
+  const uint64_t scale2 = dev::f2_pack(sl2, sl2), negm2 = dev::f2_pack(neg_m, neg_m);
+  uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+  for (int c0 = 0; c0 < NC; c0 += 32) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const int c = c0 + 2 * j;
+      const uint64_t x2 = dev::f2_fma(dev::f2_pack(s[c], s[c + 1]), scale2, negm2);
+      float x0, x1;
+      dev::f2_unpack(x2, x0, x1);
+      const float p0 = dev::ex2(x0), p1 = dev::ex2(x1);
+      acc[j & 3] = dev::f2_add(acc[j & 3], dev::f2_pack(p0, p1));
+      pk[j] = dev::pack_bf16x2(p0, p1);
+    }
+    dev::tmem_st16(s_col + (c0 >> 1), pk);
+  }
+  float sum[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) dev::f2_unpack(acc[j], sum[2 * j], sum[2 * j + 1]);
+  dev::tmem_wait_st();
+  dev::tc_fence_before();
+  dev::mbar_arrive(p_bar);
+  st.l += ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7]));
 }
 
 enum Kind : int { kNone = 0, kWhole = 1, kPart = 2 };
@@ -95,6 +214,7 @@ struct Sched {
     const int k = key0(t) + 128, e = t < sink_tiles ? se : hi;
     return k < e ? k : e;
   }
+  __device__ bool narrow(int t) const { return end(t) - key0(t) <= kNarrow; }
   __device__ int kind(int x, int t) const {
     const int k0 = key0(t), k1 = end(t);
     if (k0 > last[x] || (k0 >= sinks && k1 - 1 <= first[x] - window)) return kNone;
@@ -113,7 +233,8 @@ struct Sched {
 };
 
 __global__ void __launch_bounds__(kThreads, 1)
-cache_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, CacheArgs a) {
+cache_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_o,
+                const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, CacheArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = dev::smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -126,33 +247,7 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   const int job = blockIdx.x / a.splits;
   const int pair = job % a.blocks, unit = job / a.blocks;
   const int b = unit / a.h_kv, g = unit - b * a.h_kv;
-  const int len = dev::cache_len(a, b);
-  const int r0 = pair * 256;
-  const bool hasB = r0 + 128 < a.rows;
-
-  Sched sc;
-  {
-    const int r_last = (r0 + 256 < a.rows ? r0 + 256 : a.rows) - 1;
-    const KeyList list = dev::unit_keys(a, len, r0 / a.group, r_last / a.group);
-    sc.se = list.se;
-    sc.lo = list.lo;
-    sc.hi = list.lo + (list.total - list.se);
-    if (sc.lo <= sc.se) {   // the window begins at the end of the first keys: one segment
-      sc.se = 0;
-      sc.lo = 0;
-    }
-    sc.sink_tiles = (sc.se + 127) / 128;
-    const int tiles = sc.sink_tiles + (sc.hi - sc.lo + 127) / 128;
-    sc.t0 = (int)((int64_t)tiles * split / a.splits);
-    sc.t1 = (int)((int64_t)tiles * (split + 1) / a.splits);
-    sc.window = a.window;
-    sc.sinks = a.sinks;
-    const int a_last = hasB ? r0 + 127 : r_last;
-    sc.first[0] = dev::row_pos(a, len, r0 / a.group);
-    sc.last[0] = dev::row_pos(a, len, a_last / a.group);
-    sc.first[1] = hasB ? dev::row_pos(a, len, (r0 + 128) / a.group) : -1;
-    sc.last[1] = hasB ? dev::row_pos(a, len, r_last / a.group) : -1;
-  }
+  const int len = dev::cache_len(a, b);   // in flight over the set-up
 
   if (threadIdx.x == 0) {
     *abort_flag = dev::load_volatile(a.status) != 0 ? 1 : 0;   // an earlier failure: do nothing
@@ -169,7 +264,7 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       dev::mbar_init(bar_addr(sbase, B_SFULL + x), 1);
       dev::mbar_init(bar_addr(sbase, B_PFULL + x), 128);
       dev::mbar_init(bar_addr(sbase, B_DONE + x), 1);
-      dev::mbar_init(bar_addr(sbase, B_Q + x), 128);
+      dev::mbar_init(bar_addr(sbase, B_Q + x), 1);
     }
     dev::mbar_init(bar_addr(sbase, B_DRAIN), 1);
     dev::fence_mbar_init();
@@ -185,6 +280,54 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   if (*abort_flag) {   // uniform: written before the barrier; later failures are met in the waits
     if (warp == 1) dev::tmem_dealloc(tmem, kTmemCols);
     return;
+  }
+
+  // the row tiles: tokens [tok0, tok0 + tok_box) of sequences [seq0, seq0 + seq_box)
+  const bool hasB = 2 * pair + 1 < a.row_tiles;
+  const int seq_tiles = (a.n_q + a.tok_box - 1) / a.tok_box;   // row tiles along a sequence's tokens
+  int tok0[2], seq0[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int ti = 2 * pair + x, s = a.prefix ? ti / seq_tiles : 0;
+    seq0[x] = a.prefix ? s * a.seq_box : b;
+    tok0[x] = (ti - s * seq_tiles) * a.tok_box;
+  }
+  if (threadIdx.x == 0) {
+    const int y = g * a.group;
+    const uint32_t half = (uint32_t)(a.group * a.tok_box * a.seq_box) * 128u;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      if (x == 1 && !hasB) break;
+      const uint32_t dst = sbase + OFF_Q + x * kTileBytes, bq = bar_addr(sbase, B_Q + x);
+      dev::mbar_arrive_expect_tx(bq, 2 * half);
+      tma_load_4d(dst, &tm_q, bq, 0, y, tok0[x], seq0[x]);
+      tma_load_4d(dst + kHalfBytes, &tm_q, bq, 64, y, tok0[x], seq0[x]);
+    }
+  }
+
+  Sched sc;
+  {
+    const int end = tok0[hasB ? 1 : 0] + a.tok_box;
+    const int i_last = (end < a.n_q ? end : a.n_q) - 1;
+    const KeyList list = dev::unit_keys(a, len, tok0[0], i_last);
+    sc.se = list.se;
+    sc.lo = list.lo;
+    sc.hi = list.lo + (list.total - list.se);
+    if (sc.lo <= sc.se) {   // the window begins at the end of the first keys: one segment
+      sc.se = 0;
+      sc.lo = 0;
+    }
+    sc.sink_tiles = (sc.se + 127) / 128;
+    const int tiles = sc.sink_tiles + (sc.hi - sc.lo + 127) / 128;   // <= 2^17 + 1; splits <= 148
+    sc.t0 = a.splits == 1 ? 0 : tiles * split / a.splits;
+    sc.t1 = a.splits == 1 ? tiles : tiles * (split + 1) / a.splits;
+    sc.window = a.window;
+    sc.sinks = a.sinks;
+    const int a_end = tok0[0] + a.tok_box;
+    sc.first[0] = dev::row_pos(a, len, tok0[0]);
+    sc.last[0] = dev::row_pos(a, len, (a_end < a.n_q ? a_end : a.n_q) - 1);
+    sc.first[1] = hasB ? dev::row_pos(a, len, tok0[1]) : -1;
+    sc.last[1] = hasB ? dev::row_pos(a, len, i_last) : -1;
   }
 
   if (warp < 4) dev::regs_release<kRegsControl>();
@@ -227,12 +370,13 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         }
         ++issued_v;
         const int valid = sc.end(prev_t) - sc.key0(prev_t);
-        if (valid < 128) {   // rows behind the segment's end: whatever the cache holds there, 0 * x has to be 0
+        const int used = valid <= kNarrow ? kNarrow : 128;   // rows that the product reads
+        if (valid < used) {   // rows behind the segment's end: whatever the cache holds there, 0 * x has to be 0
           if (!warp_wait(bv, (uv / kVStages) & 1, abort_flag, a.status, 9)) {
             ok = false;
             break;
           }
-          for (int e = lane; e < (128 - valid) * 16; e += 32) {
+          for (int e = lane; e < (used - valid) * 16; e += 32) {
             const int row = valid + (e >> 4), c = e & 15;
             *reinterpret_cast<uint4*>(sgen + vbase + (c >> 3) * kHalfBytes + row * 128 + (c & 7) * 16) =
                 make_uint4(0u, 0u, 0u, 0u);
@@ -250,6 +394,8 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     }
     if (!ok) {
       // error path: let the copies already issued land before the CTA exits
+      dev::mbar_drain(bar_addr(sbase, B_Q), 0);
+      if (hasB) dev::mbar_drain(bar_addr(sbase, B_Q + 1), 0);
       for (int s = 0; s < kKStages && s < issued_k; ++s) {
         const int last = issued_k - 1 - ((issued_k - 1 - s) % kKStages);
         dev::mbar_drain(bar_addr(sbase, B_KFULL + s), (last / kKStages) & 1);
@@ -262,22 +408,27 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
     const uint32_t idesc_qk = dev::umma_idesc_bf16(128, 128, false);
+    const uint32_t idesc_narrow = dev::umma_idesc_bf16(128, kNarrow, false);
     const uint32_t idesc_pv = dev::umma_idesc_bf16(128, 128, true);
     const uint64_t QD0 = dev::smem_desc_sw128(sbase + OFF_Q, 16, 1024);
     const uint64_t KD0 = dev::smem_desc_sw128(sbase + OFF_K, 16, 1024);
     const uint64_t VD0 = dev::smem_desc_sw128(sbase + OFF_V, kHalfBytes, 1024);
     int kx0 = 0, kx1 = 0;   // P.V issued per row tile
-    auto qk = [&](int x, int u) {
+    auto qk = [&](int x, int u, bool narrow) {
       dev::umma_ss8_w(tmem + (uint32_t)x * 128u, QD0 + (uint64_t)(x * (kTileBytes >> 4)),
-                      KD0 + (uint64_t)((u % kKStages) * (kTileBytes >> 4)), idesc_qk, 0u);
+                      KD0 + (uint64_t)((u % kKStages) * (kTileBytes >> 4)), narrow ? idesc_narrow : idesc_qk, 0u);
       dev::umma_commit_w(bar_addr(sbase, B_SFULL + x));
     };
-    auto pv = [&](int x, int u) -> bool {
+    auto pv = [&](int x, int u, bool narrow) -> bool {
       const int kx = x == 0 ? kx0 : kx1;
       if (!warp_wait(bar_addr(sbase, B_PFULL + x), kx & 1, abort_flag, a.status, 4 + x)) return false;
       dev::tc_fence_after();
-      dev::umma_ts8_w(tmem + 256u + (uint32_t)x * 128u, tmem + (uint32_t)x * 128u,
-                      VD0 + (uint64_t)((u % kVStages) * (kTileBytes >> 4)), idesc_pv, kx > 0 ? 1u : 0u);
+      const uint32_t d = tmem + 256u + (uint32_t)x * 128u, p = tmem + (uint32_t)x * 128u;
+      const uint64_t vd = VD0 + (uint64_t)((u % kVStages) * (kTileBytes >> 4));
+      if (narrow)
+        umma_ts2_w(d, p, vd, idesc_pv, kx > 0 ? 1u : 0u);
+      else
+        dev::umma_ts8_w(d, p, vd, idesc_pv, kx > 0 ? 1u : 0u);
       if (x == 0) ++kx0; else ++kx1;
       return true;
     };
@@ -288,11 +439,11 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     if (have) {
       ok = warp_wait(bar_addr(sbase, B_KFULL + 0), 0, abort_flag, a.status, 6);
       dev::tc_fence_after();
-      if (ok && ka != kNone) qk(0, 0);
+      if (ok && ka != kNone) qk(0, 0, sc.narrow(t));
     }
     int u = 0;
     while (ok && have) {
-      if (kb != kNone) qk(1, u);
+      if (kb != kNone) qk(1, u, sc.narrow(t));
       dev::umma_commit_w(bar_addr(sbase, B_KEMPTY + u % kKStages));
       int t2 = t + 1, ka2 = 0, kb2 = 0;
       const bool have2 = sc.next(t2, ka2, kb2);
@@ -302,7 +453,7 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         break;
       }
       dev::tc_fence_after();
-      if (ka != kNone && !pv(0, u)) {
+      if (ka != kNone && !pv(0, u, sc.narrow(t))) {
         ok = false;
         break;
       }
@@ -313,9 +464,9 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
           break;
         }
         dev::tc_fence_after();
-        if (ka2 != kNone) qk(0, u + 1);
+        if (ka2 != kNone) qk(0, u + 1, sc.narrow(t2));
       }
-      if (kb != kNone && !pv(1, u)) {
+      if (kb != kNone && !pv(1, u, sc.narrow(t))) {
         ok = false;
         break;
       }
@@ -343,37 +494,15 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     const uint32_t s_col = tmem + lane_base + (uint32_t)x * 128;
     const uint32_t o_col = tmem + lane_base + 256u + (uint32_t)x * 128;
-    const int row = r0 + x * 128 + r;
     if (x == 0 || hasB) {
-      const bool in = row < a.rows;
-      const dev::Row w = dev::unit_row(a, b, g, in ? row : 0);
-      const int pos = in ? dev::row_pos(a, len, w.i) : -1;
-      {
-        // the tile's queries into the 128-byte swizzled layout, half a warp
-        // per row, all loads in flight at once; rows past the unit's end are zero
-        const int c = lane & 15;
-        uint4 qv[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int qr = r0 + x * 128 + quarter * 32 + e * 2 + (lane >> 4);
-          qv[e] = make_uint4(0u, 0u, 0u, 0u);
-          if (qr < a.rows) {
-            const dev::Row y = dev::unit_row(a, b, g, qr);
-            qv[e] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + y.b * a.sq.seq +
-                                                    y.h * a.sq.head + y.i * a.sq.token + c * 8);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int qr = quarter * 32 + e * 2 + (lane >> 4);
-          *reinterpret_cast<uint4*>(sgen + OFF_Q + x * kTileBytes + (c >> 3) * kHalfBytes + qr * 128 +
-                                    (((c & 7) ^ (qr & 7)) << 4)) = qv[e];
-        }
-        dev::fence_proxy_async_smem();
-        dev::mbar_arrive(bar_addr(sbase, B_Q + x));
-      }
+      // the lane's row: a (sequence, token, head of the group) of the tile's box
+      const int rest = (int)(((uint64_t)r * a.group_mul) >> 36);
+      const int ds = a.seq_box == 1 ? 0 : rest / a.tok_box;
+      const int tok = tok0[x] + rest - ds * a.tok_box;
+      const bool in = r < a.group * a.tok_box * a.seq_box && tok < a.n_q && seq0[x] + ds < a.n_seqs;
+      const int pos = in ? dev::row_pos(a, len, tok) : -1;
       const float sl2 = a.scale_log2;
-      float m_ref = -INFINITY, l = 0.f;
+      SoftRow st{-INFINITY, 0.f};
       int k = 0;
       bool ok = true;
       for (int t = sc.t0; t < sc.t1; ++t) {
@@ -384,104 +513,58 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
           break;
         }
         dev::tc_fence_after();
-        float s[128];
-        dev::tmem_ld128(s_col, s);
-        dev::tmem_wait_ld();
-        if (kind == kPart) {
-          // column c is key k0 + c: seen for low < c <= high, or c < front
-          const int k0 = sc.key0(t), e = sc.end(t) - 1;
-          const int high = (pos < e ? pos : e) - k0, low = pos - a.window - k0, front = a.sinks - k0;
-          if (front <= 0 || low < 0) {
-#pragma unroll
-            for (int c = 0; c < 128; ++c) s[c] = (c <= high && c > low) ? s[c] : -INFINITY;
-          } else {
-#pragma unroll
-            for (int c = 0; c < 128; ++c) s[c] = (c <= high && (c > low || c < front)) ? s[c] : -INFINITY;
-          }
-        }
-        float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-        for (int c = 4; c < 124; c += 8) {
-          mx[0] = dev::max3(mx[0], s[c], s[c + 1]);
-          mx[1] = dev::max3(mx[1], s[c + 2], s[c + 3]);
-          mx[2] = dev::max3(mx[2], s[c + 4], s[c + 5]);
-          mx[3] = dev::max3(mx[3], s[c + 6], s[c + 7]);
-        }
-        mx[0] = dev::max3(mx[0], s[124], s[125]);
-        mx[1] = dev::max3(mx[1], s[126], s[127]);
-        const float tmax = fmaxf(dev::max3(mx[0], mx[1], mx[2]), mx[3]) * sl2;
-        const bool need = tmax > m_ref + kRescaleLog2 || (m_ref == -INFINITY && tmax > -INFINITY);
-        const float factor = need ? dev::ex2(m_ref - tmax) : 1.f;   // 0 when m_ref = -inf
-        if (k > 0 && __any_sync(0xffffffffu, need)) {
-          // O holds P V of every earlier tile (it completed before S landed)
-#pragma unroll 1
-          for (int c0 = 0; c0 < 128; c0 += 32) {
-            uint32_t v[32];
-            dev::tmem_ld32(o_col + c0, v);
-            dev::tmem_wait_ld();
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * factor);
-            dev::tmem_st32(o_col + c0, v);
-          }
-        }
-        if (need) {
-          l *= factor;
-          m_ref = tmax;
-        }
-        const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
-        // P = 2^(x - m), rounded to bf16 for the product with V (l keeps it in
-        // fp32); chunk c0 goes to S columns [c0/2, c0/2 + 16), already consumed
-        const uint64_t scale2 = dev::f2_pack(sl2, sl2), negm2 = dev::f2_pack(neg_m, neg_m);
-        uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-        for (int c0 = 0; c0 < 128; c0 += 32) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int c = c0 + 2 * j;
-            const uint64_t x2 = dev::f2_fma(dev::f2_pack(s[c], s[c + 1]), scale2, negm2);
-            float x0, x1;
-            dev::f2_unpack(x2, x0, x1);
-            const float p0 = dev::ex2(x0), p1 = dev::ex2(x1);
-            acc[j & 3] = dev::f2_add(acc[j & 3], dev::f2_pack(p0, p1));
-            pk[j] = dev::pack_bf16x2(p0, p1);
-          }
-          dev::tmem_st16(s_col + (c0 >> 1), pk);
-        }
-        float sum[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) dev::f2_unpack(acc[j], sum[2 * j], sum[2 * j + 1]);
-        dev::tmem_wait_st();
-        dev::tc_fence_before();
-        dev::mbar_arrive(bar_addr(sbase, B_PFULL + x));
-        l += ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7]));
+        const int k0 = sc.key0(t), e = sc.end(t) - 1;
+        const int high = (pos < e ? pos : e) - k0, low = pos - a.window - k0, front = a.sinks - k0;
+        if (sc.narrow(t))
+          soft_tile<kNarrow>(st, s_col, o_col, k == 0, kind == kPart, low, high, front, sl2, bar_addr(sbase, B_PFULL + x));
+        else
+          soft_tile<128>(st, s_col, o_col, k == 0, kind == kPart, low, high, front, sl2, bar_addr(sbase, B_PFULL + x));
         ++k;
       }
       if (ok && k > 0) {
         ok = warp_wait(bar_addr(sbase, B_DONE + x), 0, abort_flag, a.status, 12 + x);
         dev::tc_fence_after();
       }
+      // Results leave through the tile's Q, which no MMA reads any more (a
+      // tile without keys has read nothing, but its load has to have landed)
+      ok = ok && warp_wait(bar_addr(sbase, B_Q + x), 0, abort_flag, a.status, 16 + x);
+      uint8_t* stage = sgen + OFF_Q + x * kTileBytes;
       if (ok && a.part_o != nullptr) {
-        const int64_t at = ((int64_t)job * a.splits + split) * 256 + x * 128 + r;
-        if (in) a.part_ml[at] = make_float2(m_ref, l);
+        // float rows, half the columns at a time through the warp's 8 KB, so
+        // that half a warp writes 256 bytes of a row
+        uint8_t* own = stage + quarter * 8192;
+        const int piece = lane & 15;
+        const int64_t at0 = ((int64_t)job * a.splits + split) * 256 + x * 128 + quarter * 32;
+        if (in) a.part_ml[at0 + lane] = make_float2(st.m_ref, st.l);
+        const uint32_t rows_in = __ballot_sync(0xffffffffu, in);
         if (k > 0) {   // without a key tile the piece has weight 0 and is not read
-          float* dst = a.part_o + at * kHeadDim;
-#pragma unroll
-          for (int c0 = 0; c0 < 128; c0 += 32) {
-            uint32_t v[32];
-            dev::tmem_ld32(o_col + c0, v);
-            dev::tmem_wait_ld();
-            if (in) {
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+#pragma unroll 1
+            for (int c0 = 0; c0 < 64; c0 += 32) {
+              uint32_t v[32];
+              dev::tmem_ld32(o_col + half * 64 + c0, v);
+              dev::tmem_wait_ld();
 #pragma unroll
               for (int j = 0; j < 8; ++j)
-                *reinterpret_cast<uint4*>(dst + c0 + 4 * j) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                *reinterpret_cast<uint4*>(own + lane * 256 + (((c0 >> 2) + j) ^ (lane & 7)) * 16) =
+                    make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
             }
+            __syncwarp();
+#pragma unroll 4
+            for (int e = 0; e < 16; ++e) {
+              const int q = e * 2 + (lane >> 4);
+              const uint4 y = *reinterpret_cast<const uint4*>(own + q * 256 + (piece ^ (q & 7)) * 16);
+              if ((rows_in >> q) & 1u)
+                *reinterpret_cast<uint4*>(a.part_o + (at0 + q) * kHeadDim + half * 64 + piece * 4) = y;
+            }
+            __syncwarp();
           }
         }
       } else if (ok) {
-        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // no key: 0; NaN stays NaN
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + w.b * a.so.seq + w.h * a.so.head + w.i * a.so.token;
-#pragma unroll
+        // bf16 rows in the box's swizzled layout, then one TMA store per half
+        const float inv = st.l > 0.f ? 1.f / st.l : (st.l == 0.f ? 0.f : st.l);   // no key: 0; NaN stays NaN
+#pragma unroll 1
         for (int c0 = 0; c0 < 128; c0 += 32) {
           uint32_t v[32];
 #pragma unroll
@@ -490,15 +573,26 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             dev::tmem_ld32(o_col + c0, v);
             dev::tmem_wait_ld();
           }
-          if (in) {
-            uint32_t y[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              y[j] = dev::pack_bf16x2(__uint_as_float(v[2 * j]) * inv, __uint_as_float(v[2 * j + 1]) * inv);
+          for (int j = 0; j < 4; ++j) {
+            uint32_t y[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              *reinterpret_cast<uint4*>(dst + c0 + 8 * j) = make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+            for (int e = 0; e < 4; ++e)
+              y[e] = dev::pack_bf16x2(__uint_as_float(v[8 * j + 2 * e]) * inv, __uint_as_float(v[8 * j + 2 * e + 1]) * inv);
+            *reinterpret_cast<uint4*>(stage + (c0 >> 6) * kHalfBytes + r * 128 + ((((c0 >> 3) + j) & 7) ^ (r & 7)) * 16) =
+                make_uint4(y[0], y[1], y[2], y[3]);
           }
+        }
+      }
+      if (a.part_o == nullptr) {
+        dev::fence_proxy_async_smem();
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + x) : "memory");   // the tile's four warps
+        if (ok && quarter == 0 && lane == 0) {
+          const uint32_t src = sbase + OFF_Q + x * kTileBytes;
+          tma_store_4d(src, &tm_o, 0, g * a.group, tok0[x], seq0[x]);
+          tma_store_4d(src + kHalfBytes, &tm_o, 64, g * a.group, tok0[x], seq0[x]);
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // before the CTA's memory goes
         }
       }
     }
@@ -511,13 +605,13 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   }
 }
 
-// Boxes of 64 columns (128 bytes) x 128 tokens of one head, 128-byte swizzle.
-bool make_cache_map(CUtensorMap* m, const void* ptr, int n, int heads, int seqs, const Strides& s) {
+// A 4-D map with boxes of 64 columns (128 bytes), 128-byte swizzle.
+bool make_map(CUtensorMap* m, const void* ptr, const int (&ext)[3], const int64_t (&stride)[3], const int (&rows)[3]) {
   auto fn = tmap_encode_fn();
   if (!fn) return false;
-  cuuint64_t dims[4] = {(cuuint64_t)kHeadDim, (cuuint64_t)n, (cuuint64_t)heads, (cuuint64_t)seqs};
-  cuuint64_t strides[3] = {(cuuint64_t)s.token * 2, (cuuint64_t)s.head * 2, (cuuint64_t)s.seq * 2};
-  cuuint32_t box[4] = {64, 128, 1, 1};
+  cuuint64_t dims[4] = {(cuuint64_t)kHeadDim, (cuuint64_t)ext[0], (cuuint64_t)ext[1], (cuuint64_t)ext[2]};
+  cuuint64_t strides[3] = {(cuuint64_t)stride[0] * 2, (cuuint64_t)stride[1] * 2, (cuuint64_t)stride[2] * 2};
+  cuuint32_t box[4] = {64, (cuuint32_t)rows[0], (cuuint32_t)rows[1], (cuuint32_t)rows[2]};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -527,15 +621,19 @@ bool make_cache_map(CUtensorMap* m, const void* ptr, int n, int heads, int seqs,
 }  // namespace
 
 cudaError_t launch_cache_tc(const CacheArgs& a, const AttnPlan& p, cudaStream_t st) {
-  CUtensorMap mk, mv;
-  if (!make_cache_map(&mk, a.k, a.n_keys, a.h_kv, a.batch, a.sk) ||
-      !make_cache_map(&mv, a.v, a.n_keys, a.h_kv, a.batch, a.sv))
+  CUtensorMap mq, mo, mk, mv;
+  const int kv[3] = {a.n_keys, a.h_kv, a.batch}, kv_box[3] = {128, 1, 1};
+  const int qo[3] = {a.h_kv * a.group, a.n_q, a.n_seqs}, qo_box[3] = {a.group, a.tok_box, a.seq_box};
+  if (!make_map(&mk, a.k, kv, {a.sk.token, a.sk.head, a.sk.seq}, kv_box) ||
+      !make_map(&mv, a.v, kv, {a.sv.token, a.sv.head, a.sv.seq}, kv_box) ||
+      !make_map(&mq, a.q, qo, {a.sq.head, a.sq.token, a.sq.seq}, qo_box) ||
+      !make_map(&mo, a.out, qo, {a.so.head, a.so.token, a.so.seq}, qo_box))
     return cudaErrorInvalidValue;
   const int64_t grid = (int64_t)p.units * p.blocks * p.splits;
   if (grid <= 0 || grid > INT32_MAX) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(cache_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
-  cache_tc_kernel<<<(unsigned)grid, kThreads, kSmemBytes, st>>>(mk, mv, a);
+  cache_tc_kernel<<<(unsigned)grid, kThreads, kSmemBytes, st>>>(mq, mo, mk, mv, a);
   return cudaGetLastError();
 }
 
