@@ -19,7 +19,8 @@ OUT = os.path.join(PKG, "libcrisp.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["api.cu", "noalloc.cu", "proxy.cu", "proxy_tc.cu", "select.cu", "pe.cu", "attn_simt.cu", "attn_tc.cu", "selftest.cu",
-           "cache_api.cu", "cache_tc.cu", "cache_tile.cu", "cache_decode.cu", "cache_merge.cu", "evict.cu"]
+           "cache_api.cu", "cache_tc.cu", "cache_tile.cu", "cache_decode.cu", "cache_decode_fp32.cu",
+           "cache_merge.cu", "evict.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I" + INCLUDE, "-I" + CSRC]

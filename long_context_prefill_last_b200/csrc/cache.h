@@ -222,6 +222,38 @@ __device__ __forceinline__ bool stair_scan(const int32_t* kv_len, int batch, int
   return __syncthreads_or(bad) != 0;
 }
 
+// A place in the flat list of key tiles that the decode kernels deal to their
+// CTAs: sequence after sequence, in each its jobs (key/value head, row block)
+// and in each job its key tiles.
+struct Place {
+  int b, jj, t;      // sequence, job within it, next key tile of the job
+  int T, len;        // key tiles of the sequence's jobs, tokens
+  KeyList list;
+  __device__ void enter(const CacheArgs& a, const int* cum) {   // after b, jj, t are set
+    T = cum[b + 1] - cum[b];
+    len = clamped_len(a, b);
+    list = unit_keys(a, len, 0, a.n_q - 1);
+  }
+  __device__ void next_job(const CacheArgs& a, const int* cum, int per_seq) {
+    t = 0;
+    if (++jj == per_seq) {
+      jj = 0;
+      do ++b; while (cum[b + 1] == cum[b]);
+      enter(a, cum);
+    }
+  }
+};
+
+// 16-byte asynchronous copy; bytes = 0 fills with zeros.
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Programmatic launch: let the next kernel of the stream start its set-up
 // early / wait until the kernels before have finished and their writes show.
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -237,6 +269,23 @@ __device__ __forceinline__ int stair_find(const int* cum, int batch, int x) {
   return lo;
 }
 
+// The start of the CTA's run of tiles, and its length (0: none).
+__device__ __forceinline__ int stair_start(const CacheArgs& a, const int* cum, Place& p) {
+  const int per_seq = a.h_kv * a.blocks;
+  const int64_t all = (int64_t)cum[a.batch] * per_seq;
+  const int64_t ctas = all < a.ctas ? all : a.ctas;            // every one of them has a tile
+  if (blockIdx.x >= ctas) return 0;
+  const int64_t x0 = all * blockIdx.x / ctas;
+  const int64_t n = all * (blockIdx.x + 1) / ctas - x0;
+  p.b = stair_find(cum, a.batch, (int)(x0 / per_seq));
+  const int64_t rem = x0 - (int64_t)cum[p.b] * per_seq;
+  const int T = cum[p.b + 1] - cum[p.b];
+  p.jj = (int)(rem / T);
+  p.t = (int)(rem - (int64_t)p.jj * T);
+  p.enter(a, cum);
+  return (int)n;
+}
+
 }  // namespace dev
 #endif
 
@@ -248,7 +297,7 @@ struct AttnPlan {
   int units;
   size_t slots;      // partial slots (0: the kernel writes the output itself)
 };
-enum AttnKernel : int { kTileSimt = 0, kDecodeMma = 1, kTileTc = 2 };
+enum AttnKernel : int { kTileSimt = 0, kDecodeMma = 1, kTileTc = 2, kDecodeSimt = 3 };
 
 struct CachePlan {
   AttnPlan main, pre;       // the sequences' own keys; the shared prefix
@@ -264,6 +313,7 @@ CachePlan plan_cache(const CacheShape& s, int op);
 // ---- launchers (each enqueues on `st`; return cudaGetLastError()) ----
 cudaError_t launch_cache_tc(const CacheArgs& a, const AttnPlan& p, cudaStream_t st);
 cudaError_t launch_cache_decode(const CacheArgs& a, const AttnPlan& p, cudaStream_t st);
+cudaError_t launch_cache_decode_fp32(const CacheArgs& a, const AttnPlan& p, cudaStream_t st);
 cudaError_t launch_cache_tile(const CacheArgs& a, const AttnPlan& p, cudaStream_t st);   // fp32
 
 struct FinishArgs {

@@ -158,20 +158,22 @@ AttnPlan plan_tc(int units, int group, int n_q, int seqs, bool prefix, int keys)
   return p;
 }
 
-// Grid of the bf16 decode kernel: two CTAs per SM, or one per key tile when
-// there are fewer.
-AttnPlan plan_decode(int units, int rows, int keys) {
+// Grid of the decode kernels: two CTAs per SM, or one per key tile when there
+// are fewer.
+AttnPlan plan_decode(int units, int rows, int keys, bool fp32) {
   AttnPlan p{};
-  p.kernel = kDecodeMma;
+  p.kernel = fp32 ? kDecodeSimt : kDecodeMma;
   p.units = units;
-  p.tile = 64;
-  p.block = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  p.tile = fp32 ? 32 : 64;
+  p.block = fp32 ? (rows <= 4 ? 4 : rows <= 8 ? 8 : 16) : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
   p.blocks = (rows + p.block - 1) / p.block;
   const int64_t jobs = (int64_t)units * p.blocks;
-  p.ctas = (int)std::min<int64_t>(2 * kSms, jobs * ((keys + 63) / 64));
+  p.ctas = (int)std::min<int64_t>(2 * kSms, jobs * ((keys + p.tile - 1) / p.tile));
   p.slots = (size_t)(jobs + p.ctas);
   return p;
 }
+
+bool decodes(const AttnPlan& p) { return p.kernel == kDecodeMma || p.kernel == kDecodeSimt; }
 
 }  // namespace
 
@@ -184,7 +186,7 @@ CachePlan plan_cache(const CacheShape& s, int op) {
     return o;
   };
   auto parts = [&](AttnPlan& a, size_t* ml, size_t* o, size_t* table) {
-    *table = take(a.kernel == kDecodeMma ? (size_t)a.units * a.blocks * 8 : 0);
+    *table = take(decodes(a) ? (size_t)a.units * a.blocks * 8 : 0);
     *ml = take(a.slots * a.block * 8);
     *o = take(a.slots * a.block * kHeadDim * 4);
   };
@@ -195,20 +197,24 @@ CachePlan plan_cache(const CacheShape& s, int op) {
     const int64_t seen = (int64_t)s.window + s.sinks + tokens - 1;
     const int keys = (int)std::min<int64_t>(s.n_k, seen);
     p.has_pre = op == CRISP_CACHE_PREFIX;
-    // fp32: the CUDA-core tiles; bf16: drafts, and a prefix that at most 64 rows
-    // read, take the decode kernel, more rows the tcgen05 tiles
+    // Few rows (a draft's, or those of all sequences for the prefix) take a
+    // decode kernel, more a tile kernel: in bf16 up to 64 rows, where the
+    // legacy tensor instruction still keeps up with memory, in fp32 up to 32,
+    // where two passes of 16 rows over the keys (80 cycles a key) beat the 64-row
+    // tile (128).
     auto plan = [&](int n_units, int n_rows, int n_keys, bool few, bool prefix) {
-      return s.fp32 ? plan_tile(n_units, n_rows, n_keys)
-             : few  ? plan_decode(n_units, n_rows, n_keys)
-                    : plan_tc(n_units, s.group, s.n_q, s.batch, prefix, n_keys);
+      return few      ? plan_decode(n_units, n_rows, n_keys, s.fp32)
+             : s.fp32 ? plan_tile(n_units, n_rows, n_keys)
+                      : plan_tc(n_units, s.group, s.n_q, s.batch, prefix, n_keys);
     };
-    p.main = plan(units, rows, keys, s.n_q <= kMaxDraft, false);
-    if (p.has_pre) p.pre = plan(s.h_kv, s.batch * rows, s.n_prefix, s.batch * rows <= 64, true);
+    const int most_rows = s.fp32 ? 32 : 64;
+    p.main = plan(units, rows, keys, s.fp32 ? rows <= most_rows : s.n_q <= kMaxDraft, false);
+    if (p.has_pre) p.pre = plan(s.h_kv, s.batch * rows, s.n_prefix, s.batch * rows <= most_rows, true);
     // output rows straight away when no row's keys are split
-    if (op == CRISP_CACHE_WINDOW && p.main.kernel != kDecodeMma && p.main.splits == 1) p.main.slots = 0;
+    if (op == CRISP_CACHE_WINDOW && !decodes(p.main) && p.main.splits == 1) p.main.slots = 0;
     // a row's pieces are read by one warp while there are few, by up to eight when there are many
     auto pieces = [](const AttnPlan& a) {
-      return a.slots == 0 ? 0 : a.kernel == kDecodeMma ? a.ctas / (a.units * a.blocks) + 1 : a.splits;
+      return a.slots == 0 ? 0 : decodes(a) ? a.ctas / (a.units * a.blocks) + 1 : a.splits;
     };
     const int most = pieces(p.main) + pieces(p.pre);
     p.warps_per_row = most > 16 ? 8 : most > 8 ? 4 : most > 4 ? 2 : 1;
@@ -238,10 +244,11 @@ crisp_status run_attention(const void* q, const void* kp, const void* vp, const 
                            cudaStream_t st) {
   int32_t* status = reinterpret_cast<int32_t*>(ws);
   // a decode kernel on its own sets the status words; otherwise they are cleared first and kernels only report
-  const bool clear = p.main.kernel != kDecodeMma || (p.has_pre && p.pre.kernel != kDecodeMma);
+  const bool clear = !decodes(p.main) || (p.has_pre && !decodes(p.pre));
   if (clear) CACHE_TRY(cudaMemsetAsync(status, 0, 32, st));
   auto launch = [&](const AttnPlan& pl, const CacheArgs& a) {
     return pl.kernel == kDecodeMma ? launch_cache_decode(a, pl, st)
+           : pl.kernel == kDecodeSimt ? launch_cache_decode_fp32(a, pl, st)
            : pl.kernel == kTileTc ? launch_cache_tc(a, pl, st)
                                   : launch_cache_tile(a, pl, st);
   };
@@ -272,7 +279,7 @@ crisp_status run_attention(const void* q, const void* kp, const void* vp, const 
     if (pl.slots == 0) return src;
     x->part_ml = reinterpret_cast<float2*>(ws + off_ml);
     x->part_o = reinterpret_cast<float*>(ws + off_o);
-    src.mode = pl.kernel == kDecodeMma ? kStair : pl.kernel == kTileTc ? kBoxes : kSplits;
+    src.mode = decodes(pl) ? kStair : pl.kernel == kTileTc ? kBoxes : kSplits;
     src.tok_box = pl.tok_box;
     src.seq_box = pl.seq_box;
     src.o = x->part_o;

@@ -40,14 +40,9 @@ constexpr uint32_t OFF_CUM = OFF_ML + 4 * 16 * 8;        // int[batch + 1]
 constexpr uint32_t smem_bytes(int batch) { return OFF_CUM + 4 * (batch + 1); }
 static_assert(2 * (smem_bytes(kMaxBatch) + 1024 + 128) <= 228 * 1024, "two CTAs per SM");
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
+using dev::cp16;
+using dev::cp_commit;
+using dev::cp_wait;
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -87,40 +82,10 @@ __global__ void __launch_bounds__(kThreads, 2) cache_decode_kernel(CacheArgs a) 
     if (a.sets_status || bad) a.status[kStatusLen] = bad ? CRISP_ERR_INVALID_ARG : 0;
   }
   const int per_seq = a.h_kv * a.blocks;                       // jobs per sequence
-  const int64_t all = (int64_t)cum[a.batch] * per_seq;
-  const int64_t ctas = all < a.ctas ? all : a.ctas;            // every one of them has a tile
-  if (blockIdx.x >= ctas) return;
-  const int64_t x0 = all * blockIdx.x / ctas;
-  const int n_all = (int)(all * (blockIdx.x + 1) / ctas - x0);
-
-  // a place in the flat tile list
-  struct Place {
-    int b, jj, t, T, len;
-    KeyList list;
-  };
-  auto enter = [&](Place& p) {   // after b, jj, t are set
-    p.T = cum[p.b + 1] - cum[p.b];
-    p.len = dev::clamped_len(a, p.b);
-    p.list = dev::unit_keys(a, p.len, 0, a.n_q - 1);
-  };
-  auto next_job = [&](Place& p) {
-    p.t = 0;
-    if (++p.jj == per_seq) {
-      p.jj = 0;
-      do ++p.b; while (cum[p.b + 1] == cum[p.b]);
-      enter(p);
-    }
-  };
-  Place ld;
-  ld.b = dev::stair_find(cum, a.batch, (int)(x0 / per_seq));
-  {
-    const int64_t rem = x0 - (int64_t)cum[ld.b] * per_seq;
-    const int T = cum[ld.b + 1] - cum[ld.b];
-    ld.jj = (int)(rem / T);
-    ld.t = (int)(rem - (int64_t)ld.jj * T);
-  }
-  enter(ld);
-  Place cp = ld;
+  dev::Place ld;
+  const int n_all = dev::stair_start(a, cum, ld);
+  if (n_all == 0) return;
+  dev::Place cp = ld;
 
   // The loads run kStages - 1 tiles ahead of the arithmetic, across jobs.
   const int lrow = tid >> 4, lchunk = tid & 15;
@@ -135,7 +100,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_decode_kernel(CacheArgs a) 
   auto load = [&]() {
     if (loaded < n_all) {
       if (ld.t == ld.T) {
-        next_job(ld);
+        ld.next_job(a, cum, per_seq);
         bind();
       }
       const uint32_t dst = sbase + (loaded % kStages) * kStageBytes + lrow * 256 + ((lchunk ^ lrow) << 4);
@@ -378,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_decode_kernel(CacheArgs a) 
     }
     done += run;
     cp.t += run;
-    if (cp.t == cp.T && done < n_all) next_job(cp);
+    if (cp.t == cp.T && done < n_all) cp.next_job(a, cum, per_seq);
   }
 }
 
