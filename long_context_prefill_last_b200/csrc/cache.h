@@ -197,9 +197,11 @@ __device__ __forceinline__ bool stair_scan(const int32_t* kv_len, int batch, int
     return __syncthreads_or(bad) != 0;
   }
   int mine = 0;
-  for (int i = 0; i < per; ++i) {
-    const int b = tid * per + i;
-    if (b < batch) mine += tiles_of(b);
+  if (per == 1) {
+    mine = tid < batch ? tiles_of(tid) : 0;
+  } else {
+    for (int i = 0; i < per; ++i)
+      if (tid * per + i < batch) mine += tiles_of(tid * per + i);
   }
   int inc = mine;
 #pragma unroll
@@ -207,16 +209,28 @@ __device__ __forceinline__ bool stair_scan(const int32_t* kv_len, int batch, int
     const int y = __shfl_up_sync(0xffffffffu, inc, d);
     if (lane >= d) inc += y;
   }
+  if (batch <= 32) {   // one warp's work
+    if (warp == 0) {
+      if (lane < batch) cum[lane] = inc - mine;
+      if (lane == 31) cum[batch] = inc;
+    }
+    return __syncthreads_or(bad) != 0;
+  }
   if (lane == 31) tmp[warp] = inc;
   __syncthreads();
   int at = inc - mine;
   for (int w = 0; w < warp; ++w) at += tmp[w];
-  for (int i = 0; i < per; ++i) {
-    const int b = tid * per + i;
-    if (b < batch) {
-      cum[b] = at;
-      at += tiles_of(b);
-      if (b == batch - 1) cum[batch] = at;
+  if (per == 1) {
+    if (tid < batch) cum[tid] = at;
+    if (tid == batch - 1) cum[batch] = at + mine;
+  } else {
+    for (int i = 0; i < per; ++i) {
+      const int b = tid * per + i;
+      if (b < batch) {
+        cum[b] = at;
+        at += tiles_of(b);
+        if (b == batch - 1) cum[batch] = at;
+      }
     }
   }
   return __syncthreads_or(bad) != 0;
@@ -269,21 +283,27 @@ __device__ __forceinline__ int stair_find(const int* cum, int batch, int x) {
   return lo;
 }
 
-// The start of the CTA's run of tiles, and its length (0: none).
-__device__ __forceinline__ int stair_start(const CacheArgs& a, const int* cum, Place& p) {
-  const int per_seq = a.h_kv * a.blocks;
-  const int64_t all = (int64_t)cum[a.batch] * per_seq;
-  const int64_t ctas = all < a.ctas ? all : a.ctas;            // every one of them has a tile
-  if (blockIdx.x >= ctas) return 0;
-  const int64_t x0 = all * blockIdx.x / ctas;
-  const int64_t n = all * (blockIdx.x + 1) / ctas - x0;
+// The start of the CTA's run of tiles, and its length (0: none): runs differ
+// by one tile at most.
+template <typename U>
+__device__ __forceinline__ int stair_run(const CacheArgs& a, const int* cum, Place& p) {
+  const U per_seq = a.h_kv * a.blocks, all = (U)cum[a.batch] * per_seq;
+  const U ctas = all < (U)a.ctas ? all : (U)a.ctas, c = blockIdx.x;   // every one of them has a tile
+  if (c >= ctas) return 0;
+  const U base = all / ctas, extra = all - base * ctas;
+  const U x0 = c * base + (c < extra ? c : extra);
   p.b = stair_find(cum, a.batch, (int)(x0 / per_seq));
-  const int64_t rem = x0 - (int64_t)cum[p.b] * per_seq;
-  const int T = cum[p.b + 1] - cum[p.b];
+  const U rem = x0 - (U)cum[p.b] * per_seq;
+  const U T = cum[p.b + 1] - cum[p.b];
   p.jj = (int)(rem / T);
-  p.t = (int)(rem - (int64_t)p.jj * T);
+  p.t = (int)(rem - (U)p.jj * T);
   p.enter(a, cum);
-  return (int)n;
+  return (int)(base + (c < extra ? 1 : 0));
+}
+__device__ __forceinline__ int stair_start(const CacheArgs& a, const int* cum, Place& p) {
+  // 64-bit divisions cost a few hundred cycles each
+  const int64_t all = (int64_t)cum[a.batch] * a.h_kv * a.blocks;
+  return all < ((int64_t)1 << 32) ? stair_run<uint32_t>(a, cum, p) : stair_run<uint64_t>(a, cum, p);
 }
 
 }  // namespace dev
