@@ -77,7 +77,8 @@ struct RowMap {
 // Where an attention launch leaves a row's partial results: runs of
 // consecutive slots of `block` rows each. kSplits: slot = job * splits + s.
 // kStair: the launch's key tiles are dealt to `ctas` CTAs as equal runs of one
-// flat list; slot = CTA + job (unique: both only grow along the list).
+// flat list; slot = (CTA + job) * splits + s (unique: CTA and job only grow
+// along the list), with `splits` results per CTA and job.
 // kBoxes: the tcgen05 kernel's row tiles, two per job; slot = job * splits + s.
 enum PartMode : int { kPartNone = 0, kSplits = 1, kStair = 2, kBoxes = 3 };
 struct PartSrc {
@@ -258,9 +259,17 @@ struct Place {
   }
 };
 
+// L2 policy for data that is read once.
+__device__ __forceinline__ uint64_t evict_first() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
 // 16-byte asynchronous copy; bytes = 0 fills with zeros.
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t bytes, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint.L2::128B [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src),
+               "r"(bytes), "l"(policy)
+               : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>

@@ -169,7 +169,8 @@ AttnPlan plan_decode(int units, int rows, int keys, bool fp32) {
   p.blocks = (rows + p.block - 1) / p.block;
   const int64_t jobs = (int64_t)units * p.blocks;
   p.ctas = (int)std::min<int64_t>(2 * kSms, jobs * ((keys + p.tile - 1) / p.tile));
-  p.slots = (size_t)(jobs + p.ctas);
+  p.splits = fp32 ? 1 : 64 / p.block;   // results per CTA and job
+  p.slots = (size_t)(jobs + p.ctas) * p.splits;
   return p;
 }
 
@@ -214,7 +215,7 @@ CachePlan plan_cache(const CacheShape& s, int op) {
     if (op == CRISP_CACHE_WINDOW && !decodes(p.main) && p.main.splits == 1) p.main.slots = 0;
     // a row's pieces are read by one warp while there are few, by up to eight when there are many
     auto pieces = [](const AttnPlan& a) {
-      return a.slots == 0 ? 0 : decodes(a) ? a.ctas / (a.units * a.blocks) + 1 : a.splits;
+      return a.slots == 0 ? 0 : decodes(a) ? (a.ctas / (a.units * a.blocks) + 1) * a.splits : a.splits;
     };
     const int most = pieces(p.main) + pieces(p.pre);
     p.warps_per_row = most > 16 ? 8 : most > 8 ? 4 : most > 4 ? 2 : 1;

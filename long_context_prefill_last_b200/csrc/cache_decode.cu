@@ -16,9 +16,12 @@
 // ring runs on across jobs. Each (CTA, job) pair leaves one partial result,
 // joined by cache_merge.cu.
 //
-// 4 warps: RT = 1, 2 or 4 of them along the rows (16 each), 4 / RT along the
-// keys of a tile; warps that share rows are joined in shared memory at the
-// end of a job's run.
+// 4 warps: RT = 1, 2 or 4 of them along the rows (16 each), KW = 4 / RT along
+// the keys of a tile, each with its own statistics and output: a run leaves KW
+// partial results per job, without a barrier between the warps at its end.
+// Keys and values, each read once, are copied with the evict-first policy,
+// which leaves the L2 cache to the logits that a scored call writes here and
+// reads in its second launch.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -33,10 +36,7 @@ constexpr int kStages = 3;
 constexpr int kThreads = 128;
 constexpr uint32_t kTileBytes = kKeys * kHeadDim * 2;   // K or V of one stage
 constexpr uint32_t kStageBytes = 2 * kTileBytes;
-constexpr int kOPitch = 64 + 4;                          // floats per row of the join buffer (half the columns)
-constexpr uint32_t OFF_JOIN = kStages * kStageBytes;     // 2 x 16 rows
-constexpr uint32_t OFF_ML = OFF_JOIN + 2 * 16 * kOPitch * 4;
-constexpr uint32_t OFF_CUM = OFF_ML + 4 * 16 * 8;        // int[batch + 1]
+constexpr uint32_t OFF_CUM = kStages * kStageBytes;      // int[batch + 1]
 constexpr uint32_t smem_bytes(int batch) { return OFF_CUM + 4 * (batch + 1); }
 static_assert(2 * (smem_bytes(kMaxBatch) + 1024 + 128) <= 228 * 1024, "two CTAs per SM");
 
@@ -89,11 +89,21 @@ __global__ void __launch_bounds__(kThreads, 2) cache_decode_kernel(CacheArgs a) 
 
   // The loads run kStages - 1 tiles ahead of the arithmetic, across jobs.
   const int lrow = tid >> 4, lchunk = tid & 15;
+  const uint64_t policy = dev::evict_first();
   const char *kp, *vp;
   auto bind = [&]() {
     const int g = ld.jj / a.blocks;
     kp = static_cast<const char*>(a.k) + (ld.b * a.sk.seq + g * a.sk.head) * 2 + lchunk * 16;
     vp = static_cast<const char*>(a.v) + (ld.b * a.sv.seq + g * a.sv.head) * 2 + lchunk * 16;
+  };
+  // the next job's queries towards the L2 cache, two tiles before they are needed
+  auto fetch_q = [&]() {
+    const int g = ld.jj / a.blocks, r = (ld.jj - g * a.blocks) * BLOCK + (tid >> 1);
+    if ((tid >> 1) < BLOCK && r < a.rows) {
+      const dev::Row w = dev::unit_row(a, ld.b, g, r);
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const __nv_bfloat16*>(a.q) + w.b * a.sq.seq +
+                                                     w.h * a.sq.head + w.i * a.sq.token + (tid & 1) * 64));
+    }
   };
   bind();
   int loaded = 0;
@@ -102,6 +112,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_decode_kernel(CacheArgs a) 
       if (ld.t == ld.T) {
         ld.next_job(a, cum, per_seq);
         bind();
+        fetch_q();
       }
       const uint32_t dst = sbase + (loaded % kStages) * kStageBytes + lrow * 256 + ((lchunk ^ lrow) << 4);
 #pragma unroll
@@ -109,8 +120,8 @@ __global__ void __launch_bounds__(kThreads, 2) cache_decode_kernel(CacheArgs a) 
         const int u = ld.t * kKeys + i * 8 + lrow;
         const bool in = u < ld.list.total;
         const int64_t j = in ? ld.list.key(u) : 0;
-        cp16(dst + i * 8 * 256, kp + j * a.sk.token * 2, in ? 16u : 0u);
-        cp16(dst + kTileBytes + i * 8 * 256, vp + j * a.sv.token * 2, in ? 16u : 0u);
+        cp16(dst + i * 8 * 256, kp + j * a.sk.token * 2, in ? 16u : 0u, policy);
+        cp16(dst + kTileBytes + i * 8 * 256, vp + j * a.sv.token * 2, in ? 16u : 0u, policy);
       }
       ++ld.t;
       ++loaded;
@@ -155,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_decode_kernel(CacheArgs a) 
 
     for (int it = 0; it < run; ++it) {
       cp_wait<kStages - 2>();
-      __syncthreads();
+      __syncthreads();   // everyone's copies have landed, and the stage that is filled next has been read
       load();
       const int t = cp.t + it;
       const uint32_t ks_base = sbase + ((done + it) % kStages) * kStageBytes, vs_base = ks_base + kTileBytes;
@@ -262,79 +273,21 @@ __global__ void __launch_bounds__(kThreads, 2) cache_decode_kernel(CacheArgs a) 
       }
     }
 
-    // join the warps that share rows: common maximum, then a tree over the
-    // warps, half the columns at a time
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
       l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
     }
-    if constexpr (KW > 1) {
-      float* buf = reinterpret_cast<float*>(smem + OFF_JOIN);
-      float2* sml = reinterpret_cast<float2*>(smem + OFF_ML);
-      if (tq == 0) {
-        sml[warp * 16 + gq] = make_float2(m[0], l[0]);
-        sml[warp * 16 + 8 + gq] = make_float2(m[1], l[1]);
-      }
-      __syncthreads();
+    const int64_t slot = ((int64_t)blockIdx.x + (int64_t)cp.b * per_seq + cp.jj) * KW + kw;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        float M = -INFINITY, L = 0.f;
+    for (int half = 0; half < 2; ++half) {
+      if (r0 + half * 8 + gq >= a.rows) continue;
+      const int64_t at = slot * BLOCK + rt * 16 + half * 8 + gq;
+      float* dst = a.part_o + at * kHeadDim + tq * 2;
 #pragma unroll
-        for (int c = 0; c < KW; ++c) M = fmaxf(M, sml[(rt + RT * c) * 16 + half * 8 + gq].x);
-        const float bs = M == -INFINITY ? 0.f : M;
-#pragma unroll
-        for (int c = 0; c < KW; ++c) {
-          const float2 ml = sml[(rt + RT * c) * 16 + half * 8 + gq];
-          L += dev::ex2(ml.x - bs) * ml.y;
-        }
-        const float w = dev::ex2(m[half] - bs);
-        m[half] = M;
-        l[half] = L;
-#pragma unroll
-        for (int n = 0; n < 16; ++n) {
-          o[n][2 * half] *= w;
-          o[n][2 * half + 1] *= w;
-        }
-      }
-#pragma unroll
-      for (int far = KW / 2; far >= 1; far >>= 1)   // warps far .. 2 far - 1 hand over to 0 .. far - 1
-#pragma unroll
-        for (int c0 = 0; c0 < 16; c0 += 8) {
-          if (kw >= far && kw < 2 * far) {
-            float* dst = buf + (((kw - far) * RT + rt) * 16 + gq) * kOPitch + tq * 2;
-#pragma unroll
-            for (int n = 0; n < 8; ++n) {
-              *reinterpret_cast<float2*>(dst + n * 8) = make_float2(o[c0 + n][0], o[c0 + n][1]);
-              *reinterpret_cast<float2*>(dst + 8 * kOPitch + n * 8) = make_float2(o[c0 + n][2], o[c0 + n][3]);
-            }
-          }
-          __syncthreads();
-          if (kw < far) {
-            const float* src = buf + ((kw * RT + rt) * 16 + gq) * kOPitch + tq * 2;
-#pragma unroll
-            for (int n = 0; n < 8; ++n) {
-              const float2 u = *reinterpret_cast<const float2*>(src + n * 8);
-              const float2 v = *reinterpret_cast<const float2*>(src + 8 * kOPitch + n * 8);
-              o[c0 + n][0] += u.x, o[c0 + n][1] += u.y;
-              o[c0 + n][2] += v.x, o[c0 + n][3] += v.y;
-            }
-          }
-          __syncthreads();
-        }
-    }
-    if (kw == 0) {
-      const int64_t slot = (int64_t)blockIdx.x + (int64_t)cp.b * per_seq + cp.jj;
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if (r0 + half * 8 + gq >= a.rows) continue;
-        const int64_t at = slot * BLOCK + rt * 16 + half * 8 + gq;
-        float* dst = a.part_o + at * kHeadDim + tq * 2;
-#pragma unroll
-        for (int n = 0; n < 16; ++n)
-          *reinterpret_cast<float2*>(dst + n * 8) = make_float2(o[n][2 * half], o[n][2 * half + 1]);
-        if (tq == 0) a.part_ml[at] = make_float2(m[half], l[half]);
-      }
+      for (int n = 0; n < 16; ++n)
+        *reinterpret_cast<float2*>(dst + n * 8) = make_float2(o[n][2 * half], o[n][2 * half + 1]);
+      if (tq == 0) a.part_ml[at] = make_float2(m[half], l[half]);
     }
     if (tid == 0) {
       int* entry = reinterpret_cast<int*>(a.table + cp.b * per_seq + cp.jj);

@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_decode_fp32_kernel(CacheArg
     vp = static_cast<const float*>(a.v) + ld.b * a.sv.seq + g * a.sv.head + lane * 4;
   };
   bind();
+  const uint64_t policy = dev::evict_first();
   int loaded = 0;
   auto load = [&]() {
     if (loaded < n_all) {
@@ -88,8 +89,8 @@ __global__ void __launch_bounds__(kThreads, 2) cache_decode_fp32_kernel(CacheArg
         const int c = i * 4 + warp, u = ld.t * kKeys + c;
         const bool in = u < ld.list.total;
         const int64_t j = in ? ld.list.key(u) : 0;
-        cp16(dst + c * kKPitch, kp + j * a.sk.token, in ? 16u : 0u);
-        cp16(dst + OFF_V + c * kVPitch, vp + j * a.sv.token, in ? 16u : 0u);
+        cp16(dst + c * kKPitch, kp + j * a.sk.token, in ? 16u : 0u, policy);
+        cp16(dst + OFF_V + c * kVPitch, vp + j * a.sv.token, in ? 16u : 0u, policy);
       }
       ++ld.t;
       ++loaded;

@@ -58,8 +58,8 @@ __device__ __forceinline__ Pieces find_pieces(const FinishArgs& a, int b, int g,
       // a job without key tiles has no entry of its own
       const bool any = src == 1 || dev::clamp_len(a.kv_len, b, a.n_k) > 0;
       const int2 ctas = any ? s.table[job] : make_int2(0, -1);
-      first = (int64_t)ctas.x + job;
-      count = ctas.y - ctas.x + 1;
+      first = ((int64_t)ctas.x + job) * s.splits;
+      count = (ctas.y - ctas.x + 1) * s.splits;
     }
     p.at[src] = first * s.block + in;
     p.count[src] = count;
@@ -73,31 +73,21 @@ __device__ __forceinline__ float2 piece_ml(const FinishArgs& a, const Pieces& p,
   return s.ml[p.at[own ? 0 : 1] + (int64_t)(own ? i : i - p.count[0]) * s.block];
 }
 
-__device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-  return x;
-}
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-  return x;
-}
-
-// Row statistics by one warp: the base that exponents subtract (0 when the row
-// sees no key) and the sum.
-__device__ __forceinline__ float2 row_stats(const FinishArgs& a, const Pieces& p, int lane) {
-  const int n = p.count[0] + p.count[1];
+// Row statistics by `lanes` neighbouring lanes (a power of two): the base that
+// exponents subtract (0 when the row sees no key) and the sum.
+__device__ __forceinline__ float2 row_stats(const FinishArgs& a, const Pieces& p, int lane, int lanes) {
+  const int n = p.count[0] + p.count[1], l0 = lane & (lanes - 1);
   float M = -INFINITY;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, piece_ml(a, p, i).x);
-  M = warp_max(M);
+  for (int i = l0; i < n; i += lanes) M = fmaxf(M, piece_ml(a, p, i).x);
+  for (int d = lanes >> 1; d >= 1; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
   const float base = M == -INFINITY ? 0.f : M;
   float L = 0.f;
-  for (int i = lane; i < n; i += 32) {
+  for (int i = l0; i < n; i += lanes) {
     const float2 ml = piece_ml(a, p, i);
     L += exp2f(ml.x - base) * ml.y;
   }
-  return make_float2(base, warp_sum(L));
+  for (int d = lanes >> 1; d >= 1; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+  return make_float2(base, L);
 }
 
 // 1 / L; 0 for a row that sees no key; NaN stays NaN.
@@ -131,7 +121,7 @@ __global__ void __launch_bounds__(kThreads) cache_finish_kernel(FinishArgs a) {
       h = bh - b * h_q;
       const int g = h / a.group, j = h - g * a.group;
       const Pieces p = find_pieces(a, b, g, i, j);
-      const float2 st = row_stats(a, p, lane);
+      const float2 st = row_stats(a, p, lane, 32);
       L = st.y;
       const int n = p.count[0] + p.count[1];
       for (int i0 = 0; i0 < n; i0 += 32) {
@@ -175,9 +165,14 @@ __global__ void __launch_bounds__(kThreads) cache_finish_kernel(FinishArgs a) {
   int u = (id - unit * a.score_ctas) * kThreads * kScoreKeys;
   if (u >= list.total) return;
   const int rows = a.n_q * a.group;
-  for (int r = warp; r < rows; r += 8) {
-    const float2 st = row_stats(a, find_pieces(a, b, g, r / a.group, r % a.group), lane);
-    if (lane == 0) fin[r] = make_float2(st.x, inverse(st.y));
+  // as many rows at once as their pieces allow: each costs a chain of loads
+  const int lanes = a.warps_per_row >= 4 ? 32 : a.warps_per_row * 4;
+  for (int r0 = 0; r0 < rows; r0 += kThreads / lanes) {   // same trips for every lane
+    const int r = r0 + (int)threadIdx.x / lanes;
+    Pieces p{{0, 0}, {0, 0}};
+    if (r < rows) p = find_pieces(a, b, g, r / a.group, r % a.group);
+    const float2 st = row_stats(a, p, lane, lanes);
+    if (r < rows && (lane & (lanes - 1)) == 0) fin[r] = make_float2(st.x, inverse(st.y));
   }
   __syncthreads();
   for (u += threadIdx.x; u < list.total; u += stride) {
