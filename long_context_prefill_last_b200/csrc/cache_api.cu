@@ -218,7 +218,7 @@ CachePlan plan_cache(const CacheShape& s, int op) {
       return a.slots == 0 ? 0 : decodes(a) ? (a.ctas / (a.units * a.blocks) + 1) * a.splits : a.splits;
     };
     const int most = pieces(p.main) + pieces(p.pre);
-    p.warps_per_row = most > 16 ? 8 : most > 8 ? 4 : most > 4 ? 2 : 1;
+    p.warps_per_row = most > 32 ? 8 : most > 16 ? 4 : most > 8 ? 2 : 1;
     parts(p.main, &p.off_ml, &p.off_o, &p.off_table);
     if (p.has_pre) parts(p.pre, &p.off_pre_ml, &p.off_pre_o, &p.off_pre_table);
     if (op == CRISP_CACHE_SCORED) {

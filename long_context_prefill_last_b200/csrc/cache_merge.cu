@@ -77,15 +77,23 @@ __device__ __forceinline__ float2 piece_ml(const FinishArgs& a, const Pieces& p,
 // exponents subtract (0 when the row sees no key) and the sum.
 __device__ __forceinline__ float2 row_stats(const FinishArgs& a, const Pieces& p, int lane, int lanes) {
   const int n = p.count[0] + p.count[1], l0 = lane & (lanes - 1);
-  float M = -INFINITY;
-  for (int i = l0; i < n; i += lanes) M = fmaxf(M, piece_ml(a, p, i).x);
-  for (int d = lanes >> 1; d >= 1; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-  const float base = M == -INFINITY ? 0.f : M;
-  float L = 0.f;
-  for (int i = l0; i < n; i += lanes) {
-    const float2 ml = piece_ml(a, p, i);
-    L += exp2f(ml.x - base) * ml.y;
+  float M = -INFINITY, L = 0.f;
+  for (int i0 = l0; i0 < n; i0 += 4 * lanes) {
+    float2 ml[4];   // four loads in flight
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      ml[e] = i0 + e * lanes < n ? piece_ml(a, p, i0 + e * lanes) : make_float2(-INFINITY, 0.f);
+    const float mn = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), M);
+    const float base = mn == -INFINITY ? 0.f : mn;
+    L *= exp2f(M - base);
+    M = mn;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) L += exp2f(ml[e].x - base) * ml[e].y;
   }
+  float top = M;
+  for (int d = lanes >> 1; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  const float base = top == -INFINITY ? 0.f : top;
+  L *= exp2f(M - base);
   for (int d = lanes >> 1; d >= 1; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
   return make_float2(base, L);
 }
@@ -128,16 +136,25 @@ __global__ void __launch_bounds__(kThreads) cache_finish_kernel(FinishArgs a) {
         float w = 0.f;
         if (i0 + lane < n) w = exp2f(piece_ml(a, p, i0 + lane).x - st.x);
         const int m = n - i0 < 32 ? n - i0 : 32;
-#pragma unroll 4
-        for (int c = part; c < m; c += W) {
-          const float f = __shfl_sync(0xffffffffu, w, c);
-          if (f == 0.f) continue;   // nothing of the piece counts (it may not even be written)
-          const int q = i0 + c;
-          const bool own = q < p.count[0];
-          const PartSrc& s = own ? a.main : a.pre;
-          const int64_t at = p.at[own ? 0 : 1] + (int64_t)(own ? q : q - p.count[0]) * s.block;
-          const float4 x = *reinterpret_cast<const float4*>(s.o + at * kHeadDim + lane * 4);
-          o.x += f * x.x, o.y += f * x.y, o.z += f * x.z, o.w += f * x.w;
+        for (int c0 = part; c0 < m; c0 += 4 * W) {
+          float4 x[4];
+          float f[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int c = c0 + e * W, q = i0 + c;
+            f[e] = __shfl_sync(0xffffffffu, w, c & 31);
+            x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (c >= m) f[e] = 0.f;
+            if (f[e] != 0.f) {   // else nothing of the piece counts (it may not even be written)
+              const bool own = q < p.count[0];
+              const PartSrc& s = own ? a.main : a.pre;
+              const int64_t at = p.at[own ? 0 : 1] + (int64_t)(own ? q : q - p.count[0]) * s.block;
+              x[e] = *reinterpret_cast<const float4*>(s.o + at * kHeadDim + lane * 4);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            o.x += f[e] * x[e].x, o.y += f[e] * x[e].y, o.z += f[e] * x[e].z, o.w += f[e] * x[e].w;
         }
       }
     }
@@ -175,37 +192,54 @@ __global__ void __launch_bounds__(kThreads) cache_finish_kernel(FinishArgs a) {
     if (r < rows && (lane & (lanes - 1)) == 0) fin[r] = make_float2(st.x, inverse(st.y));
   }
   __syncthreads();
-  for (u += threadIdx.x; u < list.total; u += stride) {
-    const float* x = a.logits + (int64_t)unit * rows * a.pitch + u;
-    float sum[kScoreKeys], old[kScoreKeys];
-    int at[kScoreKeys];   // offsets that stay inside the list
-    float* dst = a.score + (int64_t)unit * a.n_k;
+  // Steps of kScoreRows rows x kScoreKeys keys per thread; a step's loads are
+  // issued before the arithmetic of the one before.
+  const int steps = (rows + kScoreRows - 1) / kScoreRows;
+  const float* x0 = a.logits + (int64_t)unit * rows * a.pitch + threadIdx.x;
+  float* dst = a.score + (int64_t)unit * a.n_k;
+  float y[kScoreRows][kScoreKeys], next[kScoreRows][kScoreKeys], old[kScoreKeys], sum[kScoreKeys];
+  auto fetch = [&](float (&v)[kScoreRows][kScoreKeys], int base, int r0) {
+#pragma unroll
+    for (int q = 0; q < kScoreRows; ++q)
+#pragma unroll
+      for (int c = 0; c < kScoreKeys; ++c)
+        v[q][c] = base + (int)threadIdx.x + c * kThreads < list.total && r0 + q < rows
+                      ? __ldcs(x0 + (r0 + q) * a.pitch + base + c * kThreads)
+                      : -INFINITY;
+  };
+  fetch(y, u, 0);
+  while (u < list.total) {
 #pragma unroll
     for (int c = 0; c < kScoreKeys; ++c) {
+      const int at = u + (int)threadIdx.x + c * kThreads;
+      old[c] = at < list.total ? dst[list.key(at)] : 0.f;
       sum[c] = 0.f;
-      at[c] = u + c * kThreads < list.total ? c * kThreads : -1;
-      old[c] = at[c] >= 0 ? dst[list.key(u + at[c])] : 0.f;
     }
-    for (int r = 0; r < rows; r += kScoreRows) {
-      float y[kScoreRows][kScoreKeys];   // all loads of a step before any arithmetic
-#pragma unroll
-      for (int q = 0; q < kScoreRows; ++q)
-#pragma unroll
-        for (int c = 0; c < kScoreKeys; ++c)
-          y[q][c] = at[c] >= 0 && r + q < rows ? __ldcs(x + (r + q) * a.pitch + at[c]) : -INFINITY;
+    for (int n = 0; n < steps; ++n) {
+      if (n + 1 < steps)
+        fetch(next, u, (n + 1) * kScoreRows);
+      else
+        fetch(next, u + stride, 0);
 #pragma unroll
       for (int q = 0; q < kScoreRows; ++q) {
-        const float2 f = fin[r + q < rows ? r + q : r];
+        const float2 f = fin[n * kScoreRows + q < rows ? n * kScoreRows + q : 0];
 #pragma unroll
         for (int c = 0; c < kScoreKeys; ++c) {
           const float w = dev::ex2(y[q][c] - f.x) * f.y;
           sum[c] += y[q][c] == -INFINITY ? 0.f : w;   // -inf: the row does not see the key
         }
       }
+#pragma unroll
+      for (int q = 0; q < kScoreRows; ++q)
+#pragma unroll
+        for (int c = 0; c < kScoreKeys; ++c) y[q][c] = next[q][c];
     }
 #pragma unroll
-    for (int c = 0; c < kScoreKeys; ++c)
-      if (at[c] >= 0) dst[list.key(u + at[c])] = old[c] + sum[c];
+    for (int c = 0; c < kScoreKeys; ++c) {
+      const int at = u + (int)threadIdx.x + c * kThreads;
+      if (at < list.total) dst[list.key(at)] = old[c] + sum[c];
+    }
+    u += stride;
   }
 }
 
