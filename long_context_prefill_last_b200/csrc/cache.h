@@ -106,6 +106,7 @@ struct CacheArgs {
   int h_kv, group, n_q, window, sinks;
   int rows, per_seq;       // rows per unit; rows per sequence within it
   int sets_status;         // the call's only kernel that reports: it sets the status words instead of a memset
+  int chained;             // launched beside the kernel before it: it ends after that one has
   int prefix;              // rows run over every sequence, every key is seen
   int tok_box, seq_box;    // tcgen05 kernel: tokens and sequences of a row tile
   int row_tiles;           // per unit
@@ -344,6 +345,24 @@ cudaError_t launch_cache_tc(const CacheArgs& a, const AttnPlan& p, cudaStream_t 
 cudaError_t launch_cache_decode(const CacheArgs& a, const AttnPlan& p, cudaStream_t st);
 cudaError_t launch_cache_decode_fp32(const CacheArgs& a, const AttnPlan& p, cudaStream_t st);
 cudaError_t launch_cache_tile(const CacheArgs& a, const AttnPlan& p, cudaStream_t st);   // fp32
+
+// Launches a kernel that may start before the one before it in the stream has
+// finished (`beside`), or after it.
+template <typename... P, typename... A>
+inline cudaError_t launch_kernel(void (*kernel)(P...), unsigned grid, int threads, size_t smem, cudaStream_t st, bool beside,
+                                 const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = beside ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 
 struct FinishArgs {
   PartSrc main, pre;

@@ -267,6 +267,7 @@ crisp_status run_attention(const void* q, const void* kp, const void* vp, const 
   a.scale_log2 = s.scale_log2;
   a.sq = s.q;
   a.so = s.out;
+  const CacheArgs base = a;   // what the prefix's launch shares with the sequences' own
   FinishArgs m{};
   auto source = [&](const AttnPlan& pl, size_t off_ml, size_t off_o, size_t off_table, CacheArgs* x) {
     PartSrc src{};
@@ -291,20 +292,6 @@ crisp_status run_attention(const void* q, const void* kp, const void* vp, const 
     src.table = x->table = reinterpret_cast<int2*>(ws + off_table);
     return src;
   };
-  if (p.has_pre) {
-    CacheArgs x = a;
-    x.k = kp;
-    x.v = vp;
-    x.sk = s.k_prefix;
-    x.sv = s.v_prefix;
-    x.batch = 1;
-    x.n_keys = s.n_prefix;
-    x.rows = s.batch * a.per_seq;
-    x.prefix = 1;
-    x.window = kNoWindow;
-    m.pre = source(p.pre, p.off_pre_ml, p.off_pre_o, p.off_pre_table, &x);
-    CACHE_TRY(launch(p.pre, x));
-  }
   a.k = k;
   a.v = v;
   a.sk = s.k;
@@ -325,6 +312,23 @@ crisp_status run_attention(const void* q, const void* kp, const void* vp, const 
     m.score = score;
   }
   CACHE_TRY(launch(p.main, a));
+  if (p.has_pre) {
+    CacheArgs x = base;
+    x.k = kp;
+    x.v = vp;
+    x.sk = s.k_prefix;
+    x.sv = s.v_prefix;
+    x.batch = 1;
+    x.n_keys = s.n_prefix;
+    x.rows = s.batch * a.per_seq;
+    x.prefix = 1;
+    x.window = kNoWindow;
+    m.pre = source(p.pre, p.off_pre_ml, p.off_pre_o, p.off_pre_table, &x);
+    // the two read nothing of each other: the prefix may start while a decode
+    // kernel on the sequences' own keys still runs (it lets it), and ends after it
+    x.chained = decodes(p.main) && p.pre.kernel != kTileSimt ? 1 : 0;
+    CACHE_TRY(launch(p.pre, x));
+  }
   if (p.main.slots == 0) return CRISP_OK;
   m.kv_len = kv_len;
   m.batch = s.batch;

@@ -298,6 +298,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_decode_kernel(CacheArgs a) 
     cp.t += run;
     if (cp.t == cp.T && done < n_all) cp.next_job(a, cum, per_seq);
   }
+  if (a.chained) dev::wait_for_launches();
 }
 
 template <int RT>
@@ -305,8 +306,7 @@ cudaError_t launch(const CacheArgs& a, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(cache_decode_kernel<RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        smem_bytes(kMaxBatch));
   if (e != cudaSuccess) return e;
-  cache_decode_kernel<RT><<<a.ctas, kThreads, smem_bytes(a.batch), st>>>(a);
-  return cudaGetLastError();
+  return launch_kernel(cache_decode_kernel<RT>, a.ctas, kThreads, smem_bytes(a.batch), st, a.chained != 0, a);
 }
 
 }  // namespace

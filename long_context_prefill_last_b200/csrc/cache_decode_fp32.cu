@@ -227,6 +227,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_decode_fp32_kernel(CacheArg
     cp.t += run;
     if (cp.t == cp.T && done < n_all) cp.next_job(a, cum, per_seq);
   }
+  if (a.chained) dev::wait_for_launches();
 }
 
 template <int R>
@@ -234,8 +235,8 @@ cudaError_t launch(const CacheArgs& a, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(cache_decode_fp32_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)Layout<R>::cum + 4 * (kMaxBatch + 1));
   if (e != cudaSuccess) return e;
-  cache_decode_fp32_kernel<R><<<a.ctas, kThreads, Layout<R>::cum + 4 * (a.batch + 1), st>>>(a);
-  return cudaGetLastError();
+  return launch_kernel(cache_decode_fp32_kernel<R>, a.ctas, kThreads, Layout<R>::cum + 4 * (a.batch + 1), st,
+                       a.chained != 0, a);
 }
 
 }  // namespace

@@ -264,17 +264,8 @@ cudaError_t launch_cache_finish(const FinishArgs& args, cudaStream_t st) {
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
   a.out_ctas = (int)out_ctas;
   a.score_ctas = (int)score_ctas;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return a.fp32 ? cudaLaunchKernelEx(&cfg, cache_finish_kernel<float>, a)
-                : cudaLaunchKernelEx(&cfg, cache_finish_kernel<__nv_bfloat16>, a);
+  return launch_kernel(a.fp32 ? cache_finish_kernel<float> : cache_finish_kernel<__nv_bfloat16>, (unsigned)grid, kThreads, 0,
+                       st, true, a);
 }
 
 }  // namespace crisp

@@ -603,6 +603,7 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     dev::tc_fence_after();
     dev::tmem_dealloc(tmem, kTmemCols);
   }
+  if (a.chained) dev::wait_for_launches();
 }
 
 // A 4-D map with boxes of 64 columns (128 bytes), 128-byte swizzle.
@@ -633,8 +634,7 @@ cudaError_t launch_cache_tc(const CacheArgs& a, const AttnPlan& p, cudaStream_t 
   if (grid <= 0 || grid > INT32_MAX) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(cache_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
-  cache_tc_kernel<<<(unsigned)grid, kThreads, kSmemBytes, st>>>(mq, mo, mk, mv, a);
-  return cudaGetLastError();
+  return launch_kernel(cache_tc_kernel, (unsigned)grid, kThreads, kSmemBytes, st, a.chained != 0, mq, mo, mk, mv, a);
 }
 
 }  // namespace crisp
