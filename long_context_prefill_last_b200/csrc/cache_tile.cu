@@ -70,20 +70,26 @@ __global__ void __launch_bounds__(256, 2) cache_tile_kernel(CacheArgs a) {
   const float* kp = static_cast<const float*>(a.k) + b * a.sk.seq + g * a.sk.head + lane * 4;
   const float* vp = static_cast<const float*>(a.v) + b * a.sv.seq + g * a.sv.head + lane * 4;
 
+  const uint32_t ks_at = dev::smem_u32(ks) + lane * 16, vs_at = dev::smem_u32(vs) + lane * 16;
+  const uint64_t policy = dev::evict_normal();   // row blocks share the keys through L2
   for (int t = t0; t < t1; ++t) {
     __syncthreads();
+    // keys first; the values land while the logits are computed
 #pragma unroll
-    for (int c = warp; c < kKeys; c += 8) {
-      const int u = t * kKeys + c;
-      float4 kx = make_float4(0.f, 0.f, 0.f, 0.f), vx = kx;
-      if (u < list.total) {
-        const int64_t j = list.key(u);
-        kx = load4(kp + j * a.sk.token);
-        vx = load4(vp + j * a.sv.token);
+    for (int which = 0; which < 2; ++which) {
+#pragma unroll
+      for (int i = 0; i < kKeys / 8; ++i) {
+        const int c = i * 8 + warp, u = t * kKeys + c;
+        const bool in = u < list.total;
+        const int64_t j = in ? list.key(u) : 0;
+        if (which == 0)
+          dev::cp16(ks_at + c * kPitch * 4, kp + j * a.sk.token, in ? 16u : 0u, policy);
+        else
+          dev::cp16(vs_at + c * kHeadDim * 4, vp + j * a.sv.token, in ? 16u : 0u, policy);
       }
-      *reinterpret_cast<float4*>(ks + c * kPitch + lane * 4) = kx;
-      *reinterpret_cast<float4*>(vs + c * kHeadDim + lane * 4) = vx;
+      dev::cp_commit();
     }
+    dev::cp_wait<1>();
     __syncthreads();
     // logits: two partial sums (even and odd pairs of dims) per entry
     uint64_t acc[4][4];
@@ -131,7 +137,8 @@ __global__ void __launch_bounds__(256, 2) cache_tile_kernel(CacheArgs a) {
         }
       }
     }
-    __syncthreads();   // the K tile has been read by everyone
+    dev::cp_wait<0>();
+    __syncthreads();   // the K tile has been read by everyone; the values are there
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
 #pragma unroll

@@ -113,12 +113,12 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a, 
     const uint32_t bm = (1u << bits[lev]) - 1u;
     if (lev == 0) {
       int i = tid;
-      for (; i + 3 * kSelThreads < n; i += 4 * kSelThreads) {
-        float x[4];
+      for (; i + 7 * kSelThreads < n; i += 8 * kSelThreads) {
+        float x[8];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) x[q] = mine[i + q * kSelThreads];
+        for (int q = 0; q < 8; ++q) x[q] = mine[i + q * kSelThreads];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < 8; ++q) {
           const uint32_t key = score_key(x[q]);
           if (hold) cached[i + q * kSelThreads] = key;
           atomicAdd(&hist[0][key >> shift[0]], 1);
@@ -139,10 +139,20 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a, 
     // bins from the top: thread t owns bins top = last - 2t and top - 1, summed over the cluster
     const int top = kBins - 1 - 2 * tid;
     int c0 = 0, c1 = 0;
-    for (int r = 0; r < cs; ++r) {
-      const int2 c = *reinterpret_cast<const int2*>((cs > 1 ? cluster.map_shared_rank(hist[lev], r) : hist[lev]) + top - 1);
-      c0 += c.y;
-      c1 += c.x;
+    if (cs > 1) {
+      int2 c[8];   // the cluster's counts, all loads in flight at once
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        c[r] = r < cs ? *reinterpret_cast<const int2*>(cluster.map_shared_rank(hist[lev], r) + top - 1) : make_int2(0, 0);
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        c0 += c[r].y;
+        c1 += c[r].x;
+      }
+    } else {
+      const int2 c = *reinterpret_cast<const int2*>(hist[lev] + top - 1);
+      c0 = c.y;
+      c1 = c.x;
     }
     const int above = cta_scan(c0 + c1, warp_sums);
     if (above < want && above + c0 >= want) {
