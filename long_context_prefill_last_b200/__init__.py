@@ -471,30 +471,42 @@ def _expect(name, t, dtype, shape, dev):
     raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
+_TORCH = None
+
+
+def _torch_module():
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
+
+
 def _cache_call(fn, cfg, stream, names, tensors, shapes, words, args):
     """Checks the tensors (of the layer's type, with their shapes) and the words (name, tensor or None, type, shape;
     contiguous), and calls the library's `fn` with the tensors' device current, on `stream` (default: that device's
     current stream)."""
-    import torch
-    dev = tensors[0].device
-    if dev.type != "cuda":
+    torch = _TORCH
+    index = tensors[0].get_device()
+    if index < 0:
         raise ValueError("the cache operators take CUDA tensors")
     want = torch.float32 if cfg.dtype == FP32 else torch.bfloat16
     for name, t, shape in zip(names, tensors, shapes):
-        if t.dtype is not want or t.shape != shape or t.device != dev:
-            _expect(name, t, want, shape, dev)
+        if t.dtype is not want or t.shape != shape or t.get_device() != index:
+            _expect(name, t, want, shape, tensors[0].device)
     for name, t, kind, shape in words:
-        if t is not None and (t.dtype is not kind or t.shape != shape or t.device != dev or not t.is_contiguous()):
-            _expect(name, t, f"contiguous {kind}", shape, dev)
-    if cfg.workspace is not None and cfg.workspace.device != dev:
-        raise ValueError(f"the workspace is on {cfg.workspace.device}, the tensors are on {dev}")
+        if t is not None and (t.dtype is not kind or t.shape != shape or t.get_device() != index
+                              or not t.is_contiguous()):
+            _expect(name, t, f"contiguous {kind}", shape, tensors[0].device)
+    if cfg.workspace is not None and cfg.workspace.get_device() != index:
+        raise ValueError(f"the workspace is on {cfg.workspace.device}, the tensors are on {tensors[0].device}")
     ref = cfg._ref(names, tensors)
-    # torch.cuda.current_stream(dev).cuda_stream without the stream object (3 us of a small call's 15)
-    raw = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else getattr(stream, "cuda_stream", stream)
-    if dev.index == torch._C._cuda_getDevice():
+    # torch.cuda.current_stream(index).cuda_stream without the stream object (3 us of a small call's 15)
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else getattr(stream, "cuda_stream", stream)
+    if index == torch._C._cuda_getDevice():
         code = fn(*args, ref, raw)
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(index):
             code = fn(*args, ref, raw)
     if code != 0:
         raise CrispError(code, fn.__name__)
@@ -503,7 +515,7 @@ def _cache_call(fn, cfg, stream, names, tensors, shapes, words, args):
 def window_attention(q, k, v, out, cfg: CacheConfig, kv_len=None, stream=None) -> None:
     """crisp_window_attention: the newest n_q tokens of every sequence attend through a window of cfg.window keys
     (0: all) and the first cfg.sinks keys."""
-    import torch
+    torch = _torch_module()
     b = cfg.batch
     qs, ks = (b, cfg.h_q, cfg.n_q, cfg.d), (b, cfg.h_kv, cfg.n_k, cfg.d)
     _cache_call(lib().crisp_window_attention, cfg, stream, _ATTEND, (q, k, v, out), (qs, ks, ks, qs),
@@ -514,7 +526,7 @@ def window_attention(q, k, v, out, cfg: CacheConfig, kv_len=None, stream=None) -
 def scored_attention(q, k, v, out, score, cfg: CacheConfig, kv_len=None, stream=None) -> None:
     """crisp_scored_attention: window_attention for n_q <= 16 that adds every key's softmax weights to
     score (float32 [batch, h_kv, n_k])."""
-    import torch
+    torch = _torch_module()
     b = cfg.batch
     qs, ks = (b, cfg.h_q, cfg.n_q, cfg.d), (b, cfg.h_kv, cfg.n_k, cfg.d)
     _cache_call(lib().crisp_scored_attention, cfg, stream, _ATTEND, (q, k, v, out), (qs, ks, ks, qs),
@@ -525,7 +537,7 @@ def scored_attention(q, k, v, out, score, cfg: CacheConfig, kv_len=None, stream=
 def shared_prefix_attention(q, k_prefix, v_prefix, k, v, out, cfg: CacheConfig, kv_len=None, stream=None) -> None:
     """crisp_shared_prefix_attention: every sequence attends over the shared k_prefix, v_prefix
     [h_kv, n_prefix, d] and its own keys."""
-    import torch
+    torch = _torch_module()
     b = cfg.batch
     qs, ks = (b, cfg.h_q, cfg.n_q, cfg.d), (b, cfg.h_kv, cfg.n_k, cfg.d)
     ps = (cfg.h_kv, cfg.n_prefix, cfg.d)
@@ -538,7 +550,7 @@ def shared_prefix_attention(q, k_prefix, v_prefix, k, v, out, cfg: CacheConfig, 
 def evict(k, v, score, k_new, v_new, score_new, kept, new_len, cfg: CacheConfig, kv_len=None, stream=None) -> None:
     """crisp_evict: the first cfg.sinks, the last cfg.recent and the highest scored keys, cfg.budget in all, move to
     the new cache; kept (int32 [batch, h_kv, budget]) gets their old indices, new_len (int32 [batch]) the lengths."""
-    import torch
+    torch = _torch_module()
     b = cfg.batch
     ks, ns = (b, cfg.h_kv, cfg.n_k, cfg.d), (b, cfg.h_kv, cfg.n_new, cfg.d)
     i32, f32 = torch.int32, torch.float32

@@ -6,11 +6,11 @@
 // to the new cache in their old order.
 //
 // Selection: the cut is found by a radix select on order-preserving 32-bit
-// keys (11 + 11 + 10 bits, counts in shared memory), then every warp counts
-// and writes the survivors of its own contiguous stretch. One cluster of 1 to
-// 8 CTAs per head shares the counts through distributed shared memory; a head
-// is a few hundred KB of scores, read once and kept in shared memory, so this
-// is bound by the latency of its few barriers. The move is bound by HBM.
+// keys (11 + 11 + 10 bits, counts in shared memory); the counts also say how
+// many survivors each CTA has, and so where its first one goes. One cluster of
+// 1 to 8 CTAs per head shares the counts through distributed shared memory; a
+// head is a few hundred KB of scores, read once and kept in shared memory, so
+// this is bound by the latency of its few barriers. The move is bound by HBM.
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -58,14 +58,14 @@ __device__ __forceinline__ int cta_scan(int x, int* warp_sums) {
 }
 
 // One cluster per (sequence, key/value head): the indices that stay, ascending.
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a, int cs) {
+__global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictArgs a, int cs) {
   extern __shared__ uint32_t cached[];
-  __shared__ int hist[3][kBins];
+  __shared__ __align__(16) int hist[3][kBins];
   __shared__ int warp_sums[32];
   __shared__ uint32_t found_bin;
   __shared__ int found_above;
-  __shared__ int warp_above[kSelWarps], warp_ties[kSelWarps];
-  __shared__ int cta_counts[2];   // above the cut, equal to it
+  __shared__ int warp_above[kSelWarps];
+  __shared__ __align__(8) int cta_counts[2];   // above the cut, equal to it
   const cg::cluster_group cluster = cg::this_cluster();
   const int unit = blockIdx.x / cs, rank = blockIdx.x - unit * cs, b = unit / a.h_kv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -168,60 +168,90 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a, 
     want -= found_above;
     __syncthreads();
   }
-  // keys above the cut stay, and the first `want` equal to it. Each warp has
-  // a contiguous stretch: counts first, then positions.
+  // Keys above the cut stay, and the first `want` equal to it. How many of
+  // either this CTA has, for those that come after it, follows from its own counts.
   const uint32_t cut = prefix;
-  const int chunk = ((n + kSelWarps - 1) / kSelWarps + 31) & ~31;
-  const int w0 = min(n, warp * chunk), w1 = min(n, w0 + chunk);
-  int n_above = 0, n_ties = 0;
-  for (int i0 = w0; i0 < w1; i0 += 32) {
-    const bool in = i0 + lane < w1;
-    const uint32_t key = in ? key_at(i0 + lane) : 0u;
-    n_above += __popc(__ballot_sync(0xffffffffu, in && key > cut));
-    n_ties += __popc(__ballot_sync(0xffffffffu, in && key == cut));
-  }
-  if (lane == 0) {
-    warp_above[warp] = n_above;
-    warp_ties[warp] = n_ties;
-  }
-  __syncthreads();
-  int before_above = 0, before_ties = 0;
-  if (warp == 0) {
-    int x = warp_above[lane], y = warp_ties[lane];
+  if (cs > 1) {
+    int up = 0;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int p = __shfl_up_sync(0xffffffffu, x, d), q = __shfl_up_sync(0xffffffffu, y, d);
-      if (lane >= d) x += p, y += q;
+    for (int lev = 0; lev < 3; ++lev) {
+      const int bin = (int)((cut >> shift[lev]) & ((1u << bits[lev]) - 1u));
+      for (int i = tid; i < kBins; i += kSelThreads) up += i > bin ? hist[lev][i] : 0;
     }
-    warp_above[lane] = x;   // inclusive
-    warp_ties[lane] = y;
-    if (lane == 31) {
-      cta_counts[0] = x;
-      cta_counts[1] = y;
+    int total = up;
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+    if (lane == 0) warp_above[warp] = total;
+    __syncthreads();
+    if (warp == 0) {
+      total = warp_above[lane];
+#pragma unroll
+      for (int d = 16; d >= 1; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+      if (lane == 0) {
+        cta_counts[0] = total;
+        cta_counts[1] = hist[2][cut & ((1u << bits[2]) - 1u)];
+      }
     }
   }
-  if (cs > 1) cluster.sync(); else __syncthreads();
-  for (int r = 0; r < rank; ++r) {
-    const int* c = cluster.map_shared_rank(cta_counts, r);
-    before_above += c[0];
-    before_ties += c[1];
+  int before_above = 0, before_ties = 0;
+  if (cs > 1) {
+    cluster.sync();
+    int2 c[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+      c[r] = r < rank ? *reinterpret_cast<const int2*>(cluster.map_shared_rank(cta_counts, r)) : make_int2(0, 0);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      before_above += c[r].x;
+      before_ties += c[r].y;
+    }
+    cluster.sync();   // nobody reads the counts, or this CTA's totals, any more
   }
-  if (warp > 0) {
-    before_above += warp_above[warp - 1];
-    before_ties += warp_ties[warp - 1];
+  // 32 keys a word, 1024 words a round: warps set the words' bits (the counts'
+  // memory serves again), a scan gives each word its place, warps write the survivors
+  uint32_t* ups = reinterpret_cast<uint32_t*>(hist[0]);
+  uint32_t* tie = reinterpret_cast<uint32_t*>(hist[1]);
+  int2* first = reinterpret_cast<int2*>(hist[2]);   // survivors before a word: above the cut, equal to it
+  for (int base = 0; base < n; base += 32 * kSelThreads) {
+    const int words = min(kSelThreads, (n - base + 31) / 32);
+#pragma unroll 4
+    for (int w = warp; w < words; w += kSelWarps) {
+      const int i = base + w * 32 + lane;
+      const uint32_t key = i < n ? key_at(i) : 0u;
+      const uint32_t x = __ballot_sync(0xffffffffu, i < n && key > cut);
+      const uint32_t y = __ballot_sync(0xffffffffu, i < n && key == cut);
+      if (lane == 0) {
+        ups[w] = x;
+        tie[w] = y;
+      }
+    }
+    __syncthreads();
+    const uint32_t x = tid < words ? ups[tid] : 0u, y = tid < words ? tie[tid] : 0u;
+    // both prefix sums at once: a round has at most 32768 of either
+    const int both = cta_scan(__popc(x) | (__popc(y) << 16), warp_sums);
+    const int at = before_above + (both & 0xffff), t = before_ties + (int)((uint32_t)both >> 16);
+    first[tid] = make_int2(at, t);
+    __syncthreads();
+    const uint32_t lower = (1u << lane) - 1u;
+#pragma unroll 4
+    for (int w = warp; w < words; w += kSelWarps) {
+      const uint32_t xs = ups[w], ys = tie[w];
+      const int2 f = first[w];
+      const int up = f.x + __popc(xs & lower), ti = f.y + __popc(ys & lower);
+      if (((xs >> lane) & 1u) || (((ys >> lane) & 1u) && ti < want)) kept[m0 + up + min(ti, want)] = s0 + base + w * 32 + lane;
+    }
+    __syncthreads();   // the words have been read
+    if (base + 32 * kSelThreads < n) {
+      if (tid == kSelThreads - 1) {
+        cta_counts[0] = at + __popc(x);
+        cta_counts[1] = t + __popc(y);
+      }
+      __syncthreads();
+      before_above = cta_counts[0];
+      before_ties = cta_counts[1];
+      __syncthreads();
+    }
   }
-  const uint32_t lower = (1u << lane) - 1u;
-  for (int i0 = w0; i0 < w1; i0 += 32) {
-    const bool in = i0 + lane < w1;
-    const uint32_t key = in ? key_at(i0 + lane) : 0u;
-    const bool up = in && key > cut, tie = in && key == cut;
-    const uint32_t ups = __ballot_sync(0xffffffffu, up), ties = __ballot_sync(0xffffffffu, tie);
-    const int t = before_ties + __popc(ties & lower);
-    if (up || (tie && t < want)) kept[m0 + before_above + __popc(ups & lower) + min(t, want)] = s0 + i0 + lane;
-    before_above += __popc(ups);
-    before_ties += __popc(ties);
-  }
-  if (cs > 1) cluster.sync();   // nobody leaves while its counts may be read
 }
 
 // Eight kept keys per warp: their key rows, value rows and scores; the scores
