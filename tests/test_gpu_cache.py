@@ -416,3 +416,130 @@ def test_serving_run(dtype):
     o = torch.empty_like(qd)
     crisp.shared_prefix_attention(qd, kn[0, :, :200], vn[0, :, :200], ks, vs, o, c, kv_len=sl)
     close(o, *plain.attention(qd, ks, vs, sl.tolist(), k_prefix=kn[0, :, :200], v_prefix=vn[0, :, :200])[:2])
+
+
+@pytest.mark.parametrize("kind", ["normal", "ties"])
+@pytest.mark.parametrize("n", [300000, 350000])
+def test_evict_long(n, kind):
+    """Stretches of more than one round of words, and more than shared memory holds."""
+    gen = torch.Generator("cuda").manual_seed(13)
+    k, v = randn(gen, 1, 1, n, D, dtype=torch.bfloat16), randn(gen, 1, 1, n, D, dtype=torch.bfloat16)
+    score = torch.exp(2 * randn(gen, 1, 1, n))
+    if kind == "ties":
+        score = torch.floor(score / 4)
+    cfg = crisp.CacheConfig(batch=1, n_q=1, n_k=n, h_q=1, h_kv=1, sinks=5, recent=77, budget=150001, n_new=150016)
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    check_evict(k, v, score, [n], cfg, run_evict(k, v, score, lens, cfg))
+
+
+def test_offsets_past_32_bits():
+    """The last sequence of a cache whose elements number more than 2^31, in every operator."""
+    gen = torch.Generator("cuda").manual_seed(14)
+    b, hq, hkv, nk = 3, 16, 8, 1 << 20
+    k = torch.zeros(b, hkv, nk, D, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    n = 3000
+    for t in (k, v):
+        t[:, :, :n] = randn(gen, b, hkv, n, D, dtype=torch.bfloat16)
+    lens = [1, 0, n]
+    kv_len = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    small = (k[:, :, :n], v[:, :, :n])
+    for nq in (1, 40):
+        cfg = crisp.CacheConfig(batch=b, n_q=nq, n_k=nk, h_q=hq, h_kv=hkv, window=700, sinks=3)
+        q = randn(gen, b, hq, nq, D, dtype=torch.bfloat16)
+        close(run_window(q, k, v, kv_len, cfg), *plain.attention(q, *small, lens, 700, 3)[:2])
+    score = torch.zeros(b, hkv, nk, device="cuda")
+    cfg = crisp.CacheConfig(batch=b, n_q=1, n_k=nk, h_q=hq, h_kv=hkv)
+    cfg.allocate_workspace(crisp.CACHE_SCORED)
+    q = randn(gen, b, hq, 1, D, dtype=torch.bfloat16)
+    out = torch.empty_like(q)
+    crisp.scored_attention(q, k, v, out, score, cfg, kv_len=kv_len)
+    want, tol, add, add_tol = plain.attention(q, *small, lens)
+    close(out, want, tol)
+    close(score[:, :, :n], add, add_tol + plain.U * add)
+    assert (score[:, :, n:] == 0).all()
+    cfg = crisp.CacheConfig(batch=b, n_q=1, n_k=nk, h_q=hq, h_kv=hkv, sinks=3, recent=50, budget=500, n_new=512)
+    check_evict(k, v, score, lens, cfg, run_evict(k, v, score, kv_len, cfg))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_many_short_sequences(dtype):
+    """The largest batch, of caches of 0 to 40 tokens."""
+    b = 1024
+    lens = [(i * 7) % 41 for i in range(b)]
+    q, k, v, kv_len, cfg = make(dtype, b, 4, 2, 1, 40, lens, seed=15, n_prefix=33, sinks=0, recent=3, budget=20, n_new=21)
+    cfg.allocate_workspace(crisp.CACHE_SCORED)
+    score, out = torch.zeros(b, 2, 40, device="cuda"), torch.empty_like(q)
+    crisp.scored_attention(q, k, v, out, score, cfg, kv_len=kv_len)
+    want, tol, add, add_tol = plain.attention(q, k, v, lens)
+    close(out, want, tol)
+    close(score, add, add_tol + plain.U * add)
+    check_evict(k, v, score, lens, cfg, run_evict(k, v, score, kv_len, cfg))
+    gen = torch.Generator("cuda").manual_seed(16)
+    kp, vp = (randn(gen, 2, 33, D, dtype=q.dtype) for _ in range(2))
+    cfg.allocate_workspace(crisp.CACHE_PREFIX)
+    crisp.shared_prefix_attention(q, kp, vp, k, v, out, cfg, kv_len=kv_len)
+    close(out, *plain.attention(q, k, v, lens, k_prefix=kp, v_prefix=vp)[:2])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_calls_in_a_chain(dtype):
+    """Each call's output is the next one's query, and the scores run on: no kernel may start on what the one before
+    has not finished. With a wait after every call the results are the same to the bit."""
+    gen = torch.Generator("cuda").manual_seed(17)
+    t, code = DT[dtype]
+    b, hq, hkv, nk = 3, 8, 2, 700
+    k, v = randn(gen, b, hkv, nk, D, dtype=t), randn(gen, b, hkv, nk, D, dtype=t)
+    kp, vp = randn(gen, hkv, 900, D, dtype=t), randn(gen, hkv, 900, D, dtype=t)
+    q0 = randn(gen, b, hq, 2, D, dtype=t)
+    lens = torch.tensor([700, 3, 350], dtype=torch.int32, device="cuda")
+    cfg = crisp.CacheConfig(batch=b, n_q=2, n_k=nk, h_q=hq, h_kv=hkv, dtype=code)
+    pre = crisp.CacheConfig(batch=b, n_q=2, n_k=nk, h_q=hq, h_kv=hkv, dtype=code, n_prefix=900)
+    cfg.workspace = pre.workspace = torch.empty(max(crisp.cache_workspace_size(cfg, crisp.CACHE_SCORED),
+                                                    crisp.cache_workspace_size(pre, crisp.CACHE_PREFIX)),
+                                                dtype=torch.uint8, device="cuda")
+
+    def run(wait):
+        a, c = q0.clone(), torch.empty_like(q0)
+        score = torch.zeros(b, hkv, nk, device="cuda")
+        for _ in range(20):
+            crisp.scored_attention(a, k, v, c, score, cfg, kv_len=lens)
+            wait()
+            c.mul_(8)
+            crisp.shared_prefix_attention(c, kp, vp, k, v, a, pre, kv_len=lens)
+            wait()
+            crisp.window_attention(a, k, v, c, cfg, kv_len=lens)
+            wait()
+            a.copy_(c).mul_(8)
+        torch.cuda.synchronize()
+        return a, c, score
+
+    for x, y in zip(run(lambda: None), run(torch.cuda.synchronize)):
+        assert torch.equal(x, y)
+        assert torch.isfinite(x).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("b", [2, 40])
+def test_shared_prefix_captured_and_on_another_stream(dtype, b):
+    gen = torch.Generator("cuda").manual_seed(18)
+    t, code = DT[dtype]
+    hq, hkv, nk, npre = 8, 2, 60, 700
+    q, k, v, kp, vp = (randn(gen, *s, D, dtype=t) for s in ((b, hq, 1), (b, hkv, nk), (b, hkv, nk), (hkv, npre), (hkv, npre)))
+    lens = torch.full((b,), nk, dtype=torch.int32, device="cuda")
+    cfg = crisp.CacheConfig(batch=b, n_q=1, n_k=nk, h_q=hq, h_kv=hkv, dtype=code, n_prefix=npre)
+    cfg.allocate_workspace(crisp.CACHE_PREFIX)
+    out, other = torch.empty_like(q), torch.empty_like(q)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        crisp.shared_prefix_attention(q, kp, vp, k, v, out, cfg, kv_len=lens)
+    side = torch.cuda.Stream()
+    for n in (nk, 13):
+        lens.fill_(n)
+        q.copy_(randn(gen, *q.shape))
+        graph.replay()
+        side.wait_stream(torch.cuda.current_stream())
+        crisp.shared_prefix_attention(q, kp, vp, k, v, other, cfg, kv_len=lens, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(out, other)
+        close(out, *plain.attention(q, k, v, [n] * b, k_prefix=kp, v_prefix=vp)[:2])
