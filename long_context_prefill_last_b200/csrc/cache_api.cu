@@ -121,8 +121,28 @@ bool ranges_meet(const void* a, const Strides& sa, int na, const void* b, const 
   return pa < pb + bytes(sb, nb) && pb < pa + bytes(sa, na);
 }
 
-// Grid of the CUDA-core tile kernel: key lists are split until about two CTAs
-// per SM have work, with at least two key tiles in each split.
+// How many CTAs share a job's key tiles. Splitting shortens the longest CTA but
+// leaves partial results to join: measured, about 5 us for the second launch
+// and 0.2 ns per row and split. `cost` is a key tile's time in us; the splits
+// fill at most `room` CTAs. (512 tokens of 32 heads through a 128-key window:
+// 12 us in one piece, 29 us in two; a chunk of 32 tokens on 4096 keys: 63 us
+// in one, 19 us in sixteen.)
+int plan_splits(int64_t jobs, int tiles, int64_t rows, int room, double cost) {
+  int best = 1;
+  double best_us = tiles * cost;
+  const int64_t most = std::min<int64_t>(room / jobs, tiles / 2);
+  for (int s = 2; s <= most; ++s) {
+    const double us = (tiles + s - 1) / s * cost + 5.0 + 2e-4 * (double)rows * s;
+    if (us < best_us) {
+      best = s;
+      best_us = us;
+    }
+  }
+  return best;
+}
+
+// Grid of the CUDA-core tile kernel, two CTAs per SM: a 64-key tile takes 4.5 us
+// on an SM of its own, and key lists are not split beyond that use.
 AttnPlan plan_tile(int units, int rows, int keys) {
   AttnPlan p{};
   p.kernel = kTileSimt;
@@ -131,29 +151,31 @@ AttnPlan plan_tile(int units, int rows, int keys) {
   p.block = 64;
   p.blocks = (rows + 63) / 64;
   const int64_t jobs = (int64_t)units * p.blocks;
-  const int tiles = (keys + 63) / 64;
-  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({2 * kSms / jobs, tiles / 2, 64}));
+  p.splits = plan_splits(jobs, (keys + 63) / 64, (int64_t)units * rows, 2 * kSms, 4.5);
   p.slots = (size_t)jobs * p.splits;
   return p;
 }
 
-// Grid of the tcgen05 kernel: one CTA per SM and pair of row tiles; key lists
-// are split while that fills more SMs, with at least two key tiles in each
-// split. A row tile holds up to 128 rows: the group's heads of as many tokens
-// as fit (of as many sequences as fit, for the prefix).
+// Grid of the tcgen05 kernel. A row tile holds up to 128 rows: the group's
+// heads of as many tokens as fit (of as many sequences as fit, for the
+// prefix). CTAs of two row tiles read the keys once for both and run one per
+// SM; CTAs of one run two per SM and hide each other's start and end, which
+// counts while there are few key tiles. Measured on 16384 tokens of 32 heads
+// (one / two row tiles): 64 keys 127 / 148 us, 512 keys 233 / 261, 1536 keys
+// 445 / 462, 2048 keys 573 / 558, 4096 keys of 32768 tokens 2.23 / 2.15 ms.
 AttnPlan plan_tc(int units, int group, int n_q, int seqs, bool prefix, int keys) {
   AttnPlan p{};
   p.kernel = kTileTc;
   p.units = units;
   p.tile = 128;
-  p.block = 256;
+  p.block = keys <= 1792 ? 128 : 256;
   p.tok_box = std::min(n_q, 128 / group);
   p.seq_box = prefix && p.tok_box == n_q ? std::min(seqs, 128 / (group * n_q)) : 1;
   p.row_tiles = (n_q + p.tok_box - 1) / p.tok_box * (prefix ? (seqs + p.seq_box - 1) / p.seq_box : 1);
-  p.blocks = (p.row_tiles + 1) / 2;
+  p.blocks = p.block == 256 ? (p.row_tiles + 1) / 2 : p.row_tiles;
   const int64_t jobs = (int64_t)units * p.blocks;
-  const int tiles = (keys + 127) / 128;
-  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(kSms / jobs, tiles / 2));
+  p.splits = plan_splits(jobs, (keys + 127) / 128, (int64_t)units * group * n_q * (prefix ? seqs : 1),
+                         p.block == 256 ? kSms : 2 * kSms, 2.0);
   p.slots = (size_t)jobs * p.splits;
   return p;
 }

@@ -45,8 +45,8 @@ __device__ __forceinline__ Pieces find_pieces(const FinishArgs& a, int b, int g,
         ti += bt * ((a.n_q + s.tok_box - 1) / s.tok_box);
         row += (b - bt * s.seq_box) * s.tok_box * a.group;
       }
-      blk = ti >> 1;
-      in = (ti & 1) * 128 + row;
+      blk = s.block == 256 ? ti >> 1 : ti;
+      in = s.block == 256 ? (ti & 1) * 128 + row : row;
     } else {
       blk = r / s.block;
       in = r - blk * s.block;

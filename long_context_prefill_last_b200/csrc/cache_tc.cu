@@ -6,8 +6,8 @@
 //     o_r = sum_j 2^(x_rj - m_r) v_j / l_r,   x_rj = scale * log2(e) * q_r . k_j
 //
 // Bound: the tensor pipe (4 * 128 FLOP per row and key) beside the softmax's
-// issue slots. One CTA takes two row tiles of a unit (A and B, up to 128 rows
-// each) and a range of its key tiles. A row tile is a TMA box of the query
+// issue slots. One CTA takes one or two row tiles of a unit (A and B, up to 128
+// rows each) and a range of its key tiles. A row tile is a TMA box of the query
 // tensor: the group's heads x a run of tokens (x sequences, for the prefix),
 // so the query heads that share a key/value head read its tiles once, and the
 // keys that a CTA's rows span beyond the window are few (64 tokens at 4 heads
@@ -20,13 +20,14 @@
 // columns.
 //
 // Warps, TMEM columns, register split and MMA order follow attn_tc.cu:
-//   warp 0       TMA producer: Q_A, Q_B, then K (3-stage ring), V (2-stage ring); clears the
+//   warp 0       TMA producer: Q_A, Q_B, then K (3-stage ring) and V (2-stage
+//                ring; a CTA of one row tile has one stage of each); clears the
 //                V rows behind the last key of a list segment, whose weights
 //                are zero but whose content may be anything
 //   warp 1       TMEM allocation; one elected lane issues every tcgen05.mma
 //   warps 4..7   softmax of tile A, warps 8..11 of tile B (row = TMEM lane)
-// TMEM: S_A [0,128), S_B [128,256), O_A [256,384), O_B [384,512); P (bf16)
-// over the first 64 columns of S. Issue order per key tile u:
+// TMEM: S_A [0,128), S_B [128,256), O_A [256,384), O_B [384,512) (one row tile:
+// S_A [0,128), O_A [128,256)); P (bf16) over the first 64 columns of S. Issue order per key tile u:
 //     S_B(u) = Q_B K_u^T,  O_A += P_A(u) V_u,  S_A(u+1) = Q_A K_{u+1}^T,  O_B += P_B(u) V_u
 // S_X(u) landing means O_X already holds P_X(u-1) V, so a softmax warp may
 // rescale O_X then; it does when a row's maximum grew by more than 2^8.
@@ -41,40 +42,46 @@
 namespace crisp {
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kRegsControl = 64;
-constexpr int kRegsSoftmax = 216;
-static_assert(128 * kRegsControl + 256 * kRegsSoftmax <= kThreads * 168, "register split exceeds the launch");
-constexpr int kKStages = 3;
-constexpr int kVStages = 2;
 constexpr uint32_t kTileBytes = 128 * 128 * 2;   // a bf16 128x128 tile: two 64-column halves
 constexpr uint32_t kHalfBytes = 128 * 128;       // 128 rows x 128 bytes
-constexpr uint32_t OFF_Q = 0;                    // A, then B
-constexpr uint32_t OFF_K = 2 * kTileBytes;
-constexpr uint32_t OFF_V = OFF_K + kKStages * kTileBytes;
-constexpr uint32_t OFF_BAR = OFF_V + kVStages * kTileBytes;
-enum {
-  B_KFULL = 0,
-  B_KEMPTY = B_KFULL + kKStages,
-  B_VFULL = B_KEMPTY + kKStages,
-  B_VEMPTY = B_VFULL + kVStages,
-  B_VCLEAR = B_VEMPTY + kVStages,  // the rows behind a segment's end are zero (one arrival per tile)
-  B_SFULL = B_VCLEAR + kVStages,   // [2]: S_X landed
-  B_PFULL = B_SFULL + 2,           // [2]: P_X written (128 arrivals)
-  B_DONE = B_PFULL + 2,            // [2]: last P_X V landed
-  B_Q = B_DONE + 2,                // [2]: Q_X landed
-  B_DRAIN = B_Q + 2,
-  B_COUNT = B_DRAIN + 1
+
+// What a CTA of NX row tiles (1 or 2) has.
+template <int NX>
+struct Cta {
+  static constexpr int threads = 128 + 128 * NX;
+  static constexpr int per_sm = NX == 2 ? 1 : 2;
+  static constexpr int regs_launch = NX == 2 ? 168 : 128;
+  static constexpr int regs_control = NX == 2 ? 64 : 40;
+  static constexpr int regs_softmax = 216;
+  static_assert(128 * regs_control + 128 * NX * regs_softmax <= threads * regs_launch, "register split exceeds the launch");
+  static constexpr int k_stages = NX == 2 ? 3 : 1;
+  static constexpr int v_stages = NX == 2 ? 2 : 1;
+  static constexpr uint32_t off_q = 0;                    // A, then B
+  static constexpr uint32_t off_k = NX * kTileBytes;
+  static constexpr uint32_t off_v = off_k + k_stages * kTileBytes;
+  static constexpr uint32_t off_bar = off_v + v_stages * kTileBytes;
+  enum {
+    b_kfull = 0,
+    b_kempty = b_kfull + k_stages,
+    b_vfull = b_kempty + k_stages,
+    b_vempty = b_vfull + v_stages,
+    b_vclear = b_vempty + v_stages,  // the rows behind a segment's end are zero (one arrival per tile)
+    b_sfull = b_vclear + v_stages,   // [2]: S_X landed
+    b_pfull = b_sfull + 2,           // [2]: P_X written (128 arrivals)
+    b_done = b_pfull + 2,            // [2]: last P_X V landed
+    b_q = b_done + 2,                // [2]: Q_X landed
+    b_drain = b_q + 2,
+    b_count = b_drain + 1
+  };
+  static constexpr uint32_t off_tmemptr = off_bar + 8 * b_count;
+  static constexpr uint32_t off_abort = off_tmemptr + 4;
+  static constexpr uint32_t smem = off_abort + 4 + 1024;   // + slack to align the base to 1024
+  static_assert(per_sm * (smem + 1024) <= 228 * 1024, "shared memory budget");
+  static constexpr uint32_t tmem_cols = 256 * NX;          // S_X, then O_X
+  static __device__ __forceinline__ uint32_t bar(uint32_t base, int i) { return base + off_bar + 8u * i; }
 };
-constexpr uint32_t OFF_TMEMPTR = OFF_BAR + 8 * B_COUNT;
-constexpr uint32_t OFF_ABORT = OFF_TMEMPTR + 4;
-constexpr uint32_t kSmemBytes = OFF_ABORT + 4 + 1024;   // + slack to align the base to 1024
-static_assert(kSmemBytes <= 232448, "shared memory budget");
-constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.f;
 constexpr int kNarrow = 32;
-
-__device__ __forceinline__ uint32_t bar_addr(uint32_t base, int i) { return base + OFF_BAR + 8u * i; }
 
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int32_t* status,
                                           int where) {
@@ -232,15 +239,17 @@ struct Sched {
   }
 };
 
-__global__ void __launch_bounds__(kThreads, 1)
+template <int NX>
+__global__ void __launch_bounds__(Cta<NX>::threads, Cta<NX>::per_sm)
 cache_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_o,
                 const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, CacheArgs a) {
+  using C = Cta<NX>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = dev::smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
   uint8_t* sgen = smem_raw + (sbase - raw);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sgen + OFF_ABORT);
-  uint32_t* tmem_ptr_smem = reinterpret_cast<uint32_t*>(sgen + OFF_TMEMPTR);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sgen + C::off_abort);
+  uint32_t* tmem_ptr_smem = reinterpret_cast<uint32_t*>(sgen + C::off_tmemptr);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   const int split = blockIdx.x % a.splits;
@@ -251,26 +260,26 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
 
   if (threadIdx.x == 0) {
     *abort_flag = dev::load_volatile(a.status) != 0 ? 1 : 0;   // an earlier failure: do nothing
-    for (int s = 0; s < kKStages; ++s) {
-      dev::mbar_init(bar_addr(sbase, B_KFULL + s), 1);
-      dev::mbar_init(bar_addr(sbase, B_KEMPTY + s), 1);
+    for (int s = 0; s < C::k_stages; ++s) {
+      dev::mbar_init(C::bar(sbase, C::b_kfull + s), 1);
+      dev::mbar_init(C::bar(sbase, C::b_kempty + s), 1);
     }
-    for (int s = 0; s < kVStages; ++s) {
-      dev::mbar_init(bar_addr(sbase, B_VFULL + s), 1);
-      dev::mbar_init(bar_addr(sbase, B_VEMPTY + s), 1);
-      dev::mbar_init(bar_addr(sbase, B_VCLEAR + s), 1);
+    for (int s = 0; s < C::v_stages; ++s) {
+      dev::mbar_init(C::bar(sbase, C::b_vfull + s), 1);
+      dev::mbar_init(C::bar(sbase, C::b_vempty + s), 1);
+      dev::mbar_init(C::bar(sbase, C::b_vclear + s), 1);
     }
     for (int x = 0; x < 2; ++x) {
-      dev::mbar_init(bar_addr(sbase, B_SFULL + x), 1);
-      dev::mbar_init(bar_addr(sbase, B_PFULL + x), 128);
-      dev::mbar_init(bar_addr(sbase, B_DONE + x), 1);
-      dev::mbar_init(bar_addr(sbase, B_Q + x), 1);
+      dev::mbar_init(C::bar(sbase, C::b_sfull + x), 1);
+      dev::mbar_init(C::bar(sbase, C::b_pfull + x), 128);
+      dev::mbar_init(C::bar(sbase, C::b_done + x), 1);
+      dev::mbar_init(C::bar(sbase, C::b_q + x), 1);
     }
-    dev::mbar_init(bar_addr(sbase, B_DRAIN), 1);
+    dev::mbar_init(C::bar(sbase, C::b_drain), 1);
     dev::fence_mbar_init();
   }
   if (warp == 1) {
-    dev::tmem_alloc(dev::smem_u32(tmem_ptr_smem), kTmemCols);
+    dev::tmem_alloc(dev::smem_u32(tmem_ptr_smem), C::tmem_cols);
     dev::tmem_relinquish();
   }
   dev::tc_fence_before();
@@ -278,17 +287,17 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
   dev::tc_fence_after();
   const uint32_t tmem = *tmem_ptr_smem;
   if (*abort_flag) {   // uniform: written before the barrier; later failures are met in the waits
-    if (warp == 1) dev::tmem_dealloc(tmem, kTmemCols);
+    if (warp == 1) dev::tmem_dealloc(tmem, C::tmem_cols);
     return;
   }
 
   // the row tiles: tokens [tok0, tok0 + tok_box) of sequences [seq0, seq0 + seq_box)
-  const bool hasB = 2 * pair + 1 < a.row_tiles;
+  const bool hasB = NX == 2 && 2 * pair + 1 < a.row_tiles;
   const int seq_tiles = (a.n_q + a.tok_box - 1) / a.tok_box;   // row tiles along a sequence's tokens
   int tok0[2], seq0[2];
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
-    const int ti = 2 * pair + x, s = a.prefix ? ti / seq_tiles : 0;
+    const int ti = NX * pair + x, s = a.prefix ? ti / seq_tiles : 0;
     seq0[x] = a.prefix ? s * a.seq_box : b;
     tok0[x] = (ti - s * seq_tiles) * a.tok_box;
   }
@@ -298,7 +307,7 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       if (x == 1 && !hasB) break;
-      const uint32_t dst = sbase + OFF_Q + x * kTileBytes, bq = bar_addr(sbase, B_Q + x);
+      const uint32_t dst = sbase + C::off_q + x * kTileBytes, bq = C::bar(sbase, C::b_q + x);
       dev::mbar_arrive_expect_tx(bq, 2 * half);
       tma_load_4d(dst, &tm_q, bq, 0, y, tok0[x], seq0[x]);
       tma_load_4d(dst + kHalfBytes, &tm_q, bq, 64, y, tok0[x], seq0[x]);
@@ -330,7 +339,7 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     sc.last[1] = hasB ? dev::row_pos(a, len, i_last) : -1;
   }
 
-  if (warp < 4) dev::regs_release<kRegsControl>();
+  if (warp < 4) dev::regs_release<C::regs_control>();
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
     if (lane == 0) {
@@ -343,36 +352,39 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     while (ok && (more || prev_t >= 0)) {
       more = more && sc.next(t, ka, kb);
       if (more) {   // K of tile u
-        const int s = u % kKStages;
-        if (!warp_wait(bar_addr(sbase, B_KEMPTY + s), ((u / kKStages) & 1) ^ 1, abort_flag, a.status, 1)) {
+        const int s = u % C::k_stages;
+        if (!warp_wait(C::bar(sbase, C::b_kempty + s), ((u / C::k_stages) & 1) ^ 1, abort_flag, a.status, 1)) {
           ok = false;
           break;
         }
         if (lane == 0) {
-          const uint32_t bk = bar_addr(sbase, B_KFULL + s);
+          const uint32_t bk = C::bar(sbase, C::b_kfull + s);
           dev::mbar_arrive_expect_tx(bk, kTileBytes);
-          tma_load_4d(sbase + OFF_K + s * kTileBytes, &tm_k, bk, 0, sc.key0(t), g, b);
-          tma_load_4d(sbase + OFF_K + s * kTileBytes + kHalfBytes, &tm_k, bk, 64, sc.key0(t), g, b);
+          tma_load_4d(sbase + C::off_k + s * kTileBytes, &tm_k, bk, 0, sc.key0(t), g, b);
+          tma_load_4d(sbase + C::off_k + s * kTileBytes + kHalfBytes, &tm_k, bk, 64, sc.key0(t), g, b);
         }
         ++issued_k;
       }
-      if (prev_t >= 0) {   // V of tile u-1
-        const int uv = u - 1, s = uv % kVStages;
-        const uint32_t vbase = OFF_V + s * kTileBytes, bv = bar_addr(sbase, B_VFULL + s);
-        if (!warp_wait(bar_addr(sbase, B_VEMPTY + s), ((uv / kVStages) & 1) ^ 1, abort_flag, a.status, 2)) {
+      // V of the tile before, whose weights are still being computed; with one
+      // stage of each, of this tile: it waits for the product before it alone
+      const int tv = NX == 1 ? (more ? t : -1) : prev_t;
+      if (tv >= 0) {
+        const int uv = NX == 1 ? u : u - 1, s = uv % C::v_stages;
+        const uint32_t vbase = C::off_v + s * kTileBytes, bv = C::bar(sbase, C::b_vfull + s);
+        if (!warp_wait(C::bar(sbase, C::b_vempty + s), ((uv / C::v_stages) & 1) ^ 1, abort_flag, a.status, 2)) {
           ok = false;
           break;
         }
         if (lane == 0) {
           dev::mbar_arrive_expect_tx(bv, kTileBytes);
-          tma_load_4d(sbase + vbase, &tm_v, bv, 0, sc.key0(prev_t), g, b);
-          tma_load_4d(sbase + vbase + kHalfBytes, &tm_v, bv, 64, sc.key0(prev_t), g, b);
+          tma_load_4d(sbase + vbase, &tm_v, bv, 0, sc.key0(tv), g, b);
+          tma_load_4d(sbase + vbase + kHalfBytes, &tm_v, bv, 64, sc.key0(tv), g, b);
         }
         ++issued_v;
-        const int valid = sc.end(prev_t) - sc.key0(prev_t);
+        const int valid = sc.end(tv) - sc.key0(tv);
         const int used = valid <= kNarrow ? kNarrow : 128;   // rows that the product reads
         if (valid < used) {   // rows behind the segment's end: whatever the cache holds there, 0 * x has to be 0
-          if (!warp_wait(bv, (uv / kVStages) & 1, abort_flag, a.status, 9)) {
+          if (!warp_wait(bv, (uv / C::v_stages) & 1, abort_flag, a.status, 9)) {
             ok = false;
             break;
           }
@@ -384,9 +396,9 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
           dev::fence_proxy_async_smem();
           __syncwarp();
         }
-        if (lane == 0) dev::mbar_arrive(bar_addr(sbase, B_VCLEAR + s));
+        if (lane == 0) dev::mbar_arrive(C::bar(sbase, C::b_vclear + s));
       }
-      prev_t = more ? t : -1;
+      prev_t = NX == 2 && more ? t : -1;
       if (more) {
         ++t;
         ++u;
@@ -394,15 +406,15 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     }
     if (!ok) {
       // error path: let the copies already issued land before the CTA exits
-      dev::mbar_drain(bar_addr(sbase, B_Q), 0);
-      if (hasB) dev::mbar_drain(bar_addr(sbase, B_Q + 1), 0);
-      for (int s = 0; s < kKStages && s < issued_k; ++s) {
-        const int last = issued_k - 1 - ((issued_k - 1 - s) % kKStages);
-        dev::mbar_drain(bar_addr(sbase, B_KFULL + s), (last / kKStages) & 1);
+      dev::mbar_drain(C::bar(sbase, C::b_q), 0);
+      if (hasB) dev::mbar_drain(C::bar(sbase, C::b_q + 1), 0);
+      for (int s = 0; s < C::k_stages && s < issued_k; ++s) {
+        const int last = issued_k - 1 - ((issued_k - 1 - s) % C::k_stages);
+        dev::mbar_drain(C::bar(sbase, C::b_kfull + s), (last / C::k_stages) & 1);
       }
-      for (int s = 0; s < kVStages && s < issued_v; ++s) {
-        const int last = issued_v - 1 - ((issued_v - 1 - s) % kVStages);
-        dev::mbar_drain(bar_addr(sbase, B_VFULL + s), (last / kVStages) & 1);
+      for (int s = 0; s < C::v_stages && s < issued_v; ++s) {
+        const int last = issued_v - 1 - ((issued_v - 1 - s) % C::v_stages);
+        dev::mbar_drain(C::bar(sbase, C::b_vfull + s), (last / C::v_stages) & 1);
       }
     }
   } else if (warp == 1) {
@@ -410,21 +422,21 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     const uint32_t idesc_qk = dev::umma_idesc_bf16(128, 128, false);
     const uint32_t idesc_narrow = dev::umma_idesc_bf16(128, kNarrow, false);
     const uint32_t idesc_pv = dev::umma_idesc_bf16(128, 128, true);
-    const uint64_t QD0 = dev::smem_desc_sw128(sbase + OFF_Q, 16, 1024);
-    const uint64_t KD0 = dev::smem_desc_sw128(sbase + OFF_K, 16, 1024);
-    const uint64_t VD0 = dev::smem_desc_sw128(sbase + OFF_V, kHalfBytes, 1024);
+    const uint64_t QD0 = dev::smem_desc_sw128(sbase + C::off_q, 16, 1024);
+    const uint64_t KD0 = dev::smem_desc_sw128(sbase + C::off_k, 16, 1024);
+    const uint64_t VD0 = dev::smem_desc_sw128(sbase + C::off_v, kHalfBytes, 1024);
     int kx0 = 0, kx1 = 0;   // P.V issued per row tile
     auto qk = [&](int x, int u, bool narrow) {
       dev::umma_ss8_w(tmem + (uint32_t)x * 128u, QD0 + (uint64_t)(x * (kTileBytes >> 4)),
-                      KD0 + (uint64_t)((u % kKStages) * (kTileBytes >> 4)), narrow ? idesc_narrow : idesc_qk, 0u);
-      dev::umma_commit_w(bar_addr(sbase, B_SFULL + x));
+                      KD0 + (uint64_t)((u % C::k_stages) * (kTileBytes >> 4)), narrow ? idesc_narrow : idesc_qk, 0u);
+      dev::umma_commit_w(C::bar(sbase, C::b_sfull + x));
     };
     auto pv = [&](int x, int u, bool narrow) -> bool {
       const int kx = x == 0 ? kx0 : kx1;
-      if (!warp_wait(bar_addr(sbase, B_PFULL + x), kx & 1, abort_flag, a.status, 4 + x)) return false;
+      if (!warp_wait(C::bar(sbase, C::b_pfull + x), kx & 1, abort_flag, a.status, 4 + x)) return false;
       dev::tc_fence_after();
-      const uint32_t d = tmem + 256u + (uint32_t)x * 128u, p = tmem + (uint32_t)x * 128u;
-      const uint64_t vd = VD0 + (uint64_t)((u % kVStages) * (kTileBytes >> 4));
+      const uint32_t d = tmem + (uint32_t)(NX + x) * 128u, p = tmem + (uint32_t)x * 128u;
+      const uint64_t vd = VD0 + (uint64_t)((u % C::v_stages) * (kTileBytes >> 4));
       if (narrow)
         umma_ts2_w(d, p, vd, idesc_pv, kx > 0 ? 1u : 0u);
       else
@@ -433,22 +445,22 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       return true;
     };
     int t = sc.t0, ka = 0, kb = 0;
-    bool ok = warp_wait(bar_addr(sbase, B_Q), 0, abort_flag, a.status, 14) &&
-              (!hasB || warp_wait(bar_addr(sbase, B_Q + 1), 0, abort_flag, a.status, 15));
+    bool ok = warp_wait(C::bar(sbase, C::b_q), 0, abort_flag, a.status, 14) &&
+              (!hasB || warp_wait(C::bar(sbase, C::b_q + 1), 0, abort_flag, a.status, 15));
     bool have = ok && sc.next(t, ka, kb);
     if (have) {
-      ok = warp_wait(bar_addr(sbase, B_KFULL + 0), 0, abort_flag, a.status, 6);
+      ok = warp_wait(C::bar(sbase, C::b_kfull + 0), 0, abort_flag, a.status, 6);
       dev::tc_fence_after();
       if (ok && ka != kNone) qk(0, 0, sc.narrow(t));
     }
     int u = 0;
     while (ok && have) {
       if (kb != kNone) qk(1, u, sc.narrow(t));
-      dev::umma_commit_w(bar_addr(sbase, B_KEMPTY + u % kKStages));
+      dev::umma_commit_w(C::bar(sbase, C::b_kempty + u % C::k_stages));
       int t2 = t + 1, ka2 = 0, kb2 = 0;
       const bool have2 = sc.next(t2, ka2, kb2);
-      if (!warp_wait(bar_addr(sbase, B_VFULL + u % kVStages), (u / kVStages) & 1, abort_flag, a.status, 7) ||
-          !warp_wait(bar_addr(sbase, B_VCLEAR + u % kVStages), (u / kVStages) & 1, abort_flag, a.status, 3)) {
+      if (!warp_wait(C::bar(sbase, C::b_vfull + u % C::v_stages), (u / C::v_stages) & 1, abort_flag, a.status, 7) ||
+          !warp_wait(C::bar(sbase, C::b_vclear + u % C::v_stages), (u / C::v_stages) & 1, abort_flag, a.status, 3)) {
         ok = false;
         break;
       }
@@ -458,7 +470,7 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         break;
       }
       if (have2) {
-        if (!warp_wait(bar_addr(sbase, B_KFULL + (u + 1) % kKStages), ((u + 1) / kKStages) & 1, abort_flag, a.status,
+        if (!warp_wait(C::bar(sbase, C::b_kfull + (u + 1) % C::k_stages), ((u + 1) / C::k_stages) & 1, abort_flag, a.status,
                        8)) {
           ok = false;
           break;
@@ -470,7 +482,7 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         ok = false;
         break;
       }
-      dev::umma_commit_w(bar_addr(sbase, B_VEMPTY + u % kVStages));
+      dev::umma_commit_w(C::bar(sbase, C::b_vempty + u % C::v_stages));
       t = t2;
       ka = ka2;
       kb = kb2;
@@ -478,22 +490,22 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       ++u;
     }
     if (ok) {
-      dev::umma_commit_w(bar_addr(sbase, B_DONE + 0));
-      dev::umma_commit_w(bar_addr(sbase, B_DONE + 1));
+      dev::umma_commit_w(C::bar(sbase, C::b_done + 0));
+      dev::umma_commit_w(C::bar(sbase, C::b_done + 1));
     }
     // every MMA issued must complete before TMEM is released
-    dev::umma_commit_w(bar_addr(sbase, B_DRAIN));
-    dev::mbar_drain(bar_addr(sbase, B_DRAIN), 0);
+    dev::umma_commit_w(C::bar(sbase, C::b_drain));
+    dev::mbar_drain(C::bar(sbase, C::b_drain), 0);
     __syncwarp();
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- softmax warps
-    dev::regs_acquire<kRegsSoftmax>();
+    dev::regs_acquire<C::regs_softmax>();
     const int x = (warp - 4) >> 2;                // 0: tile A, 1: tile B
     const int quarter = warp & 3;                 // TMEM lane quarter of this warp
     const int r = quarter * 32 + lane;            // row inside the tile
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     const uint32_t s_col = tmem + lane_base + (uint32_t)x * 128;
-    const uint32_t o_col = tmem + lane_base + 256u + (uint32_t)x * 128;
+    const uint32_t o_col = tmem + lane_base + (uint32_t)(NX + x) * 128;
     if (x == 0 || hasB) {
       // the lane's row: a (sequence, token, head of the group) of the tile's box
       const int rest = (int)(((uint64_t)r * a.group_mul) >> 36);
@@ -508,7 +520,7 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       for (int t = sc.t0; t < sc.t1; ++t) {
         const int kind = sc.kind(x, t);
         if (kind == kNone) continue;
-        if (!warp_wait(bar_addr(sbase, B_SFULL + x), k & 1, abort_flag, a.status, 10 + x)) {
+        if (!warp_wait(C::bar(sbase, C::b_sfull + x), k & 1, abort_flag, a.status, 10 + x)) {
           ok = false;
           break;
         }
@@ -516,25 +528,25 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         const int k0 = sc.key0(t), e = sc.end(t) - 1;
         const int high = (pos < e ? pos : e) - k0, low = pos - a.window - k0, front = a.sinks - k0;
         if (sc.narrow(t))
-          soft_tile<kNarrow>(st, s_col, o_col, k == 0, kind == kPart, low, high, front, sl2, bar_addr(sbase, B_PFULL + x));
+          soft_tile<kNarrow>(st, s_col, o_col, k == 0, kind == kPart, low, high, front, sl2, C::bar(sbase, C::b_pfull + x));
         else
-          soft_tile<128>(st, s_col, o_col, k == 0, kind == kPart, low, high, front, sl2, bar_addr(sbase, B_PFULL + x));
+          soft_tile<128>(st, s_col, o_col, k == 0, kind == kPart, low, high, front, sl2, C::bar(sbase, C::b_pfull + x));
         ++k;
       }
       if (ok && k > 0) {
-        ok = warp_wait(bar_addr(sbase, B_DONE + x), 0, abort_flag, a.status, 12 + x);
+        ok = warp_wait(C::bar(sbase, C::b_done + x), 0, abort_flag, a.status, 12 + x);
         dev::tc_fence_after();
       }
       // Results leave through the tile's Q, which no MMA reads any more (a
       // tile without keys has read nothing, but its load has to have landed)
-      ok = ok && warp_wait(bar_addr(sbase, B_Q + x), 0, abort_flag, a.status, 16 + x);
-      uint8_t* stage = sgen + OFF_Q + x * kTileBytes;
+      ok = ok && warp_wait(C::bar(sbase, C::b_q + x), 0, abort_flag, a.status, 16 + x);
+      uint8_t* stage = sgen + C::off_q + x * kTileBytes;
       if (ok && a.part_o != nullptr) {
         // float rows, half the columns at a time through the warp's 8 KB, so
         // that half a warp writes 256 bytes of a row
         uint8_t* own = stage + quarter * 8192;
         const int piece = lane & 15;
-        const int64_t at0 = ((int64_t)job * a.splits + split) * 256 + x * 128 + quarter * 32;
+        const int64_t at0 = ((int64_t)job * a.splits + split) * (128 * NX) + x * 128 + quarter * 32;
         if (in) a.part_ml[at0 + lane] = make_float2(st.m_ref, st.l);
         const uint32_t rows_in = __ballot_sync(0xffffffffu, in);
         if (k > 0) {   // without a key tile the piece has weight 0 and is not read
@@ -588,7 +600,7 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         dev::fence_proxy_async_smem();
         asm volatile("bar.sync %0, 128;" ::"r"(1 + x) : "memory");   // the tile's four warps
         if (ok && quarter == 0 && lane == 0) {
-          const uint32_t src = sbase + OFF_Q + x * kTileBytes;
+          const uint32_t src = sbase + C::off_q + x * kTileBytes;
           tma_store_4d(src, &tm_o, 0, g * a.group, tok0[x], seq0[x]);
           tma_store_4d(src + kHalfBytes, &tm_o, 64, g * a.group, tok0[x], seq0[x]);
           asm volatile("cp.async.bulk.commit_group;" ::: "memory");
@@ -601,7 +613,7 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
   __syncthreads();
   if (warp == 1) {
     dev::tc_fence_after();
-    dev::tmem_dealloc(tmem, kTmemCols);
+    dev::tmem_dealloc(tmem, C::tmem_cols);
   }
   if (a.chained) dev::wait_for_launches();
 }
@@ -632,9 +644,12 @@ cudaError_t launch_cache_tc(const CacheArgs& a, const AttnPlan& p, cudaStream_t 
     return cudaErrorInvalidValue;
   const int64_t grid = (int64_t)p.units * p.blocks * p.splits;
   if (grid <= 0 || grid > INT32_MAX) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(cache_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  const auto kernel = p.block == 256 ? cache_tc_kernel<2> : cache_tc_kernel<1>;
+  const int smem = p.block == 256 ? Cta<2>::smem : Cta<1>::smem;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_kernel(cache_tc_kernel, (unsigned)grid, kThreads, kSmemBytes, st, a.chained != 0, mq, mo, mk, mv, a);
+  return launch_kernel(kernel, (unsigned)grid, p.block == 256 ? Cta<2>::threads : Cta<1>::threads, smem, st,
+                       a.chained != 0, mq, mo, mk, mv, a);
 }
 
 }  // namespace crisp
