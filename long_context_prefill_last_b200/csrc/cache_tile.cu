@@ -10,6 +10,10 @@
 // tx + 16 j, and output columns 4 tx .. 4 tx + 3 and 64 + 4 tx .. of the same
 // rows. A row of a unit is a (token, head of the group) pair, so a key tile is
 // read once for all query heads that share it.
+//
+// Bound: FMA and shared memory (12 wavefronts of loads per 32 packed FMA in the
+// logits, 20 per 32 in the output). Measured: 4096 tokens of one head through a
+// 512-key window in 50 us, 62% of the FMA pipe on SMs that hold two CTAs.
 #include <math.h>
 
 #include "cache.h"
