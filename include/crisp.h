@@ -286,7 +286,8 @@ typedef enum { CRISP_CACHE_WINDOW = 0, CRISP_CACHE_SCORED = 1, CRISP_CACHE_PREFI
 crisp_status crisp_cache_cfg_init(crisp_cache_cfg* cfg, int32_t batch, int32_t n_q, int32_t n_k, int32_t h_q,
                                   int32_t h_kv, int32_t d, int32_t dtype);
 
-/* Workspace bytes that operator `op` needs for cfg's shape (strides do not matter). */
+/* Workspace bytes that operator `op` needs for cfg's shape (strides do not matter).
+ * A scored call keeps 4 bytes per query row and key slot that a row can see. */
 crisp_status crisp_cache_workspace_size(const crisp_cache_cfg* cfg, int32_t op, size_t* bytes);
 
 /* Attention with a sliding window and first tokens that stay visible: whole

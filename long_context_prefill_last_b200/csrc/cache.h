@@ -117,7 +117,7 @@ struct CacheArgs {
   // partial results (NULL: write the output rows)
   float* part_o;
   float2* part_ml;
-  int block, blocks, splits, ctas;
+  int block, blocks, splits, ctas;   // block: rows of a partial slot
   int2* table;             // decode kernel: [job] first and last CTA that had a tile of it
   // scored: scaled logits [unit][row][pitch] by list index
   float* logits;
@@ -328,6 +328,7 @@ __device__ __forceinline__ int stair_start(const CacheArgs& a, const int* cum, P
 struct AttnPlan {
   int kernel;        // AttnKernel
   int block, blocks, splits, ctas, tile;
+  int slot_rows;     // rows of a partial slot: the block's, or the unit's where it has only one block
   int tok_box, seq_box, row_tiles;   // kTileTc
   int units;
   size_t slots;      // partial slots (0: the kernel writes the output itself)

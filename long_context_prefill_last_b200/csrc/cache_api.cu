@@ -148,7 +148,7 @@ AttnPlan plan_tile(int units, int rows, int keys) {
   p.kernel = kTileSimt;
   p.units = units;
   p.tile = 64;
-  p.block = 64;
+  p.block = p.slot_rows = 64;
   p.blocks = (rows + 63) / 64;
   const int64_t jobs = (int64_t)units * p.blocks;
   p.splits = plan_splits(jobs, (keys + 63) / 64, (int64_t)units * rows, 2 * kSms, 4.5);
@@ -168,7 +168,7 @@ AttnPlan plan_tc(int units, int group, int n_q, int seqs, bool prefix, int keys)
   p.kernel = kTileTc;
   p.units = units;
   p.tile = 128;
-  p.block = keys <= 1792 ? 128 : 256;
+  p.block = p.slot_rows = keys <= 1792 ? 128 : 256;
   p.tok_box = std::min(n_q, 128 / group);
   p.seq_box = prefix && p.tok_box == n_q ? std::min(seqs, 128 / (group * n_q)) : 1;
   p.row_tiles = (n_q + p.tok_box - 1) / p.tok_box * (prefix ? (seqs + p.seq_box - 1) / p.seq_box : 1);
@@ -189,6 +189,7 @@ AttnPlan plan_decode(int units, int rows, int keys, bool fp32) {
   p.tile = fp32 ? 32 : 64;
   p.block = fp32 ? (rows <= 4 ? 4 : rows <= 8 ? 8 : 16) : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
   p.blocks = (rows + p.block - 1) / p.block;
+  p.slot_rows = std::min(p.block, rows);
   const int64_t jobs = (int64_t)units * p.blocks;
   p.ctas = (int)std::min<int64_t>(2 * kSms, jobs * ((keys + p.tile - 1) / p.tile));
   p.splits = fp32 ? 1 : 64 / p.block;   // results per CTA and job
@@ -210,8 +211,8 @@ CachePlan plan_cache(const CacheShape& s, int op) {
   };
   auto parts = [&](AttnPlan& a, size_t* ml, size_t* o, size_t* table) {
     *table = take(decodes(a) ? (size_t)a.units * a.blocks * 8 : 0);
-    *ml = take(a.slots * a.block * 8);
-    *o = take(a.slots * a.block * kHeadDim * 4);
+    *ml = take(a.slots * a.slot_rows * 8);
+    *o = take(a.slots * a.slot_rows * kHeadDim * 4);
   };
   if (op != CRISP_CACHE_EVICT) {
     const int units = s.batch * s.h_kv, rows = s.n_q * s.group;
@@ -293,7 +294,7 @@ crisp_status run_attention(const void* q, const void* kp, const void* vp, const 
   FinishArgs m{};
   auto source = [&](const AttnPlan& pl, size_t off_ml, size_t off_o, size_t off_table, CacheArgs* x) {
     PartSrc src{};
-    x->block = pl.block;
+    x->block = pl.slot_rows;
     x->blocks = pl.blocks;
     x->splits = pl.splits;
     x->ctas = pl.ctas;
@@ -308,7 +309,7 @@ crisp_status run_attention(const void* q, const void* kp, const void* vp, const 
     src.seq_box = pl.seq_box;
     src.o = x->part_o;
     src.ml = x->part_ml;
-    src.block = pl.block;
+    src.block = pl.slot_rows;
     src.blocks = pl.blocks;
     src.splits = pl.splits;
     src.table = x->table = reinterpret_cast<int2*>(ws + off_table);

@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_decode_kernel(CacheArgs a) 
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       if (r0 + half * 8 + gq >= a.rows) continue;
-      const int64_t at = slot * BLOCK + rt * 16 + half * 8 + gq;
+      const int64_t at = slot * a.block + rt * 16 + half * 8 + gq;
       float* dst = a.part_o + at * kHeadDim + tq * 2;
 #pragma unroll
       for (int n = 0; n < 16; ++n)

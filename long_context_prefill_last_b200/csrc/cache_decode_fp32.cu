@@ -215,11 +215,11 @@ __global__ void __launch_bounds__(kThreads, 2) cache_decode_fp32_kernel(CacheArg
     const int64_t slot = (int64_t)blockIdx.x + (int64_t)cp.b * per_seq + cp.jj;
 #pragma unroll
     for (int r = 0; r < R; ++r)
-      if (rb * R + r < a.rows) a.part_o[(slot * R + r) * kHeadDim + tid] = o[r];
+      if (rb * R + r < a.rows) a.part_o[(slot * a.block + r) * kHeadDim + tid] = o[r];
 #pragma unroll
     for (int i = 0; i < RW; ++i) {
       const int r = i * 4 + warp;
-      if (lane == 0 && rb * R + r < a.rows) a.part_ml[slot * R + r] = make_float2(m[i], l[i]);
+      if (lane == 0 && rb * R + r < a.rows) a.part_ml[slot * a.block + r] = make_float2(m[i], l[i]);
     }
     if (tid == 0) {
       int* entry = reinterpret_cast<int*>(a.table + cp.b * per_seq + cp.jj);
