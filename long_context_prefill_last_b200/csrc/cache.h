@@ -106,6 +106,7 @@ struct CacheArgs {
   int h_kv, group, n_q, window, sinks;
   int rows, per_seq;       // rows per unit; rows per sequence within it
   int sets_status;         // the call's only kernel that reports: it sets the status words instead of a memset
+  int cluster;             // bf16 decode kernel: CTAs of a cluster that has a job to itself (0: runs of the flat list)
   int chained;             // launched beside the kernel before it: it ends after that one has
   int prefix;              // rows run over every sequence, every key is seen
   int tok_box, seq_box;    // tcgen05 kernel: tokens and sequences of a row tile
@@ -122,6 +123,7 @@ struct CacheArgs {
   // scored: scaled logits [unit][row][pitch] by list index
   float* logits;
   int64_t pitch;
+  float* score;            // [batch][h_kv][n_keys]
 };
 
 #ifdef __CUDACC__
@@ -331,6 +333,7 @@ struct AttnPlan {
   int slot_rows;     // rows of a partial slot: the block's, or the unit's where it has only one block
   int tok_box, seq_box, row_tiles;   // kTileTc
   int units;
+  int cluster;       // kDecodeMma: CTAs per job that join their results themselves (0: see kStair)
   size_t slots;      // partial slots (0: the kernel writes the output itself)
 };
 enum AttnKernel : int { kTileSimt = 0, kDecodeMma = 1, kTileTc = 2, kDecodeSimt = 3 };
@@ -352,22 +355,36 @@ cudaError_t launch_cache_decode(const CacheArgs& a, const AttnPlan& p, cudaStrea
 cudaError_t launch_cache_decode_fp32(const CacheArgs& a, const AttnPlan& p, cudaStream_t st);
 cudaError_t launch_cache_tile(const CacheArgs& a, const AttnPlan& p, cudaStream_t st);   // fp32
 
-// Launches a kernel that may start before the one before it in the stream has
-// finished (`beside`), or after it.
+// Launches a kernel in clusters of `cluster` CTAs; with `beside` it may start
+// before the one before it in the stream has finished.
 template <typename... P, typename... A>
-inline cudaError_t launch_kernel(void (*kernel)(P...), unsigned grid, int threads, size_t smem, cudaStream_t st, bool beside,
-                                 const A&... args) {
+inline cudaError_t launch_clusters(void (*kernel)(P...), unsigned grid, unsigned cluster, int threads, size_t smem,
+                                   cudaStream_t st, bool beside, const A&... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = beside ? 1 : 0;
+  cudaLaunchAttribute attr[2] = {};
+  unsigned n = 0;
+  if (beside) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = cluster;
+    attr[n].val.clusterDim.y = 1;
+    attr[n++].val.clusterDim.z = 1;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+template <typename... P, typename... A>
+inline cudaError_t launch_kernel(void (*kernel)(P...), unsigned grid, int threads, size_t smem, cudaStream_t st, bool beside,
+                                 const A&... args) {
+  return launch_clusters(kernel, grid, 1, threads, smem, st, beside, args...);
 }
 
 struct FinishArgs {
