@@ -30,8 +30,8 @@
 //
 // Measured: one token of 32 query and 8 key/value heads on 524288 tokens, 2.15
 // GB of keys and values and 67 MB of logits in 326 us (6.8 TB/s); 125 MB of
-// windows of 32 sequences in 27 us (4.6 TB/s: 3 us until the first copies are
-// under way, 14 tiles per CTA).
+// windows of 32 sequences in 27 us a call (4.7 TB/s: 3 us until the first
+// copies are under way, 17 tiles per CTA).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <math.h>
