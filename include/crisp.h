@@ -318,8 +318,9 @@ crisp_status crisp_shared_prefix_attention(const void* q, const void* k_prefix, 
  * [batch][h_kv][n_new]); later scores become 0, later keys and values are left
  * as they were. kept (int32 [batch][h_kv][budget]) gets the old indices,
  * ascending, then -1; new_len (int32 [batch], not kv_len itself) the lengths.
- * The new cache must not overlap the old one (CRISP_ERR_INVALID_ARG). n_q,
- * window and sm_scale are not used. */
+ * The new cache must not overlap the old one; the address ranges from their
+ * first to their last element are compared (CRISP_ERR_INVALID_ARG). n_q, window
+ * and sm_scale are not used. */
 crisp_status crisp_evict(const void* k, const void* v, const float* score, const int32_t* kv_len, void* k_new,
                          void* v_new, float* score_new, int32_t* kept, int32_t* new_len,
                          const crisp_cache_cfg* cfg, void* stream);

@@ -57,10 +57,11 @@ static_assert(2 * (smem_bytes(kMaxBatch) + 1024 + 128) <= 228 * 1024, "two CTAs 
 constexpr int kOPitch = kHeadDim + 4;
 constexpr uint32_t OFF_WO = 0;                                   // float[4][16][kOPitch]
 constexpr uint32_t OFF_WML = OFF_WO + 4 * 16 * kOPitch * 4;      // float2[4][16]
-constexpr uint32_t OFF_CO = OFF_WML + 4 * 16 * 8;                // float[64][128]
-constexpr uint32_t OFF_CML = OFF_CO + 64 * kHeadDim * 4;         // float2[64]
-constexpr uint32_t OFF_FIN = OFF_CML + 64 * 8;                   // float2[64]
-static_assert(OFF_FIN + 64 * 8 <= OFF_CUM, "the join aliases the ring");
+constexpr int kClusterRows = 32;                                 // rows of a cluster's job
+constexpr uint32_t OFF_CO = OFF_WML + 4 * 16 * 8;                // float[kClusterRows][128]
+constexpr uint32_t OFF_CML = OFF_CO + kClusterRows * kHeadDim * 4;   // float2[kClusterRows]
+constexpr uint32_t OFF_FIN = OFF_CML + kClusterRows * 8;         // float2[kClusterRows]
+static_assert(OFF_FIN + kClusterRows * 8 <= OFF_CUM, "the join aliases the ring");
 
 using dev::cp16;
 using dev::cp_commit;
@@ -454,11 +455,18 @@ __global__ void __launch_bounds__(kThreads, 2) cache_decode_kernel(CacheArgs a) 
 
 template <int RT>
 cudaError_t launch(const CacheArgs& a, const AttnPlan& p, cudaStream_t st) {
-  const auto kernel = p.cluster > 0 ? cache_decode_kernel<RT, true> : cache_decode_kernel<RT, false>;
+  if constexpr (16 * RT <= kClusterRows) {
+    if (p.cluster > 0) {
+      const auto kernel = cache_decode_kernel<RT, true>;
+      cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(1));
+      if (e != cudaSuccess) return e;
+      return launch_clusters(kernel, (unsigned)(p.units * p.cluster), p.cluster, kThreads, smem_bytes(1), st, false, a);
+    }
+  }
+  if (p.cluster > 0) return cudaErrorInvalidValue;
+  const auto kernel = cache_decode_kernel<RT, false>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(kMaxBatch));
   if (e != cudaSuccess) return e;
-  if (p.cluster > 0)
-    return launch_clusters(kernel, (unsigned)(p.units * p.cluster), p.cluster, kThreads, smem_bytes(1), st, false, a);
   return launch_kernel(kernel, a.ctas, kThreads, smem_bytes(a.batch), st, a.chained != 0, a);
 }
 
