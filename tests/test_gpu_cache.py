@@ -543,3 +543,28 @@ def test_shared_prefix_captured_and_on_another_stream(dtype, b):
         torch.cuda.current_stream().wait_stream(side)
         assert torch.equal(out, other)
         close(out, *plain.attention(q, k, v, [n] * b, k_prefix=kp, v_prefix=vp)[:2])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("nq", [40, 5])
+def test_lengths_outside_the_cache_in_every_kernel(dtype, nq):
+    """Prompt and flat-list kernels, and eviction: clamped to [0, n_k], reported once."""
+    nk, lens = 4200, [1 << 30, -5, 100]
+    q, k, v, _, cfg = make(dtype, 3, 16, 1, nq, nk, [nk, nk, nk], seed=21, window=300, sinks=2, recent=4, budget=70, n_new=70)
+    kv_len = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    k.nan_to_num_(0.5), v.nan_to_num_(0.5, 0.5, 0.5)
+    out, check = guarded(*q.shape, dtype=q.dtype)
+    cfg.allocate_workspace(crisp.CACHE_WINDOW)
+    crisp.window_attention(q, k, v, out, cfg, kv_len=kv_len)
+    assert crisp.cache_device_status(cfg) == 1 and crisp.cache_device_status(cfg) == 0
+    check()
+    real = [nk, 0, 100]
+    close(out, *plain.attention(q, k, v, real, 300, 2)[:2])
+    score = torch.rand(3, 1, nk, device="cuda")
+    cfg.allocate_workspace(crisp.CACHE_EVICT)
+    got = [torch.full((3, 1, 70, D), 7.0, dtype=k.dtype, device="cuda") for _ in range(2)]
+    got += [torch.zeros(3, 1, 70, device="cuda"), torch.zeros(3, 1, 70, dtype=torch.int32, device="cuda"),
+            torch.zeros(3, dtype=torch.int32, device="cuda")]
+    crisp.evict(k, v, score, *got, cfg, kv_len=kv_len)
+    assert crisp.cache_device_status(cfg) == 1
+    check_evict(k, v, score, real, cfg, got)
