@@ -1,0 +1,45 @@
+"""Paths of the cache operators that single out a kernel form, on the GPU
+against the definitions in 64 bits (tests/cache_plain.py derives the
+tolerances; tests/test_cache_plans.py checks that the shapes take the path)."""
+import pytest
+
+import cache_plain as plain
+import cache_shapes as shapes
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+import long_context_prefill_last_b200 as crisp  # noqa: E402
+from test_gpu_cache import D, built, close, guarded, make, randn, run_window  # noqa: E402, F401
+
+
+@pytest.mark.parametrize("case", [c for c, _ in shapes.TWO_TILES], ids=lambda c: "-".join(map(str, c)).replace(" ", ""))
+def test_window_with_two_row_tiles(case):
+    b, hq, hkv, nq, nk, lens, window, sinks = case
+    q, k, v, kv_len, cfg = make("bf16", b, hq, hkv, nq, nk, lens, seed=30, window=window, sinks=sinks)
+    out = run_window(q, k, v, kv_len, cfg)
+    want, tol, _, _ = plain.attention(q, k, v, lens, window, sinks)
+    close(out, want, tol)
+    for s in range(b):
+        empty = max(0, min(nq, nq - lens[s]))
+        assert (out[s, :, :empty] == 0).all()
+    assert torch.equal(out, run_window(q, k, v, kv_len, cfg))
+
+
+def test_token_major_layout_with_two_row_tiles():
+    gen = torch.Generator("cuda").manual_seed(31)
+    b, hq, hkv, nq, nk = 2, 14, 2, 1900, 2300
+    q = randn(gen, b, nq, hq, D, dtype=torch.bfloat16).transpose(1, 2)
+    kv = randn(gen, b, nk + 7, hkv, 2 * D, dtype=torch.bfloat16)[:, 7:].transpose(1, 2)
+    k, v = kv[..., :D], kv[..., D:]
+    buf, check = guarded(b, nq, hq, D, dtype=torch.bfloat16)
+    out = buf.transpose(1, 2)
+    cfg = crisp.CacheConfig(batch=b, n_q=nq, n_k=nk, h_q=hq, h_kv=hkv, window=1850, sinks=33)
+    cfg.allocate_workspace(crisp.CACHE_WINDOW)
+    crisp.window_attention(q, k, v, out, cfg)
+    assert crisp.cache_device_status(cfg) == 0
+    check()
+    close(out, *plain.attention(q, k, v, [nk] * b, 1850, 33)[:2])
