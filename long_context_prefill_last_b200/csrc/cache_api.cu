@@ -197,21 +197,36 @@ AttnPlan plan_decode(int units, int rows, int keys, bool fp32) {
   return p;
 }
 
-// A cluster per job instead of runs of the flat list and a second launch: where
-// it keeps a CTA's share of a full cache within kClusterMore tiles of the flat
-// list's, and for up to 32 rows, whose join is short. Measured in us on the GPU
-// (cluster / flat list), 32 query and 8 key/value heads, one token: 1 sequence
-// of 512 keys 5.6 / 7.5, 4 of 2048 10.0 / 13.9, 32 of 1024 22.5 / 28.6; 28 and 4
-// heads, 3 tokens (21 rows): 8 of 1024 11.8 / 14.6; 64 rows: 2 of 1024 15.4 /
-// 10.7. The host saves another 2 us.
+// A cluster per job instead of runs of the flat list and a second launch, for up
+// to 32 rows, whose join is short. The lengths are not known here, so two
+// things bound a CTA's share of a full cache: it stays within kClusterMore tiles
+// of the flat list's, for sequences of like lengths, and within kClusterTiles
+// tiles of 16 rows, for a long one among short ones, where the flat list deals
+// its tiles to every SM and a cluster walks them alone. Measured in us (cluster /
+// flat list; 32 query and 8 key/value heads, one token, 64-key tiles of a CTA in
+// brackets), every sequence full, lengths even from 1 up, and one full sequence
+// among others of 64 tokens:
+//   37 x  512 keys [8]    22 / 29     18 / 29     16 / 20
+//   32 x 1024 keys [16]   31 / 37     27 / 33     22 / 22
+//   32 x 2048 keys [32]   51 / 59     41 / 45     37 / 31
+//   37 x 8192 keys [128] 199 / 205   139 / 117   117 / 49
+// 74 sequences, 4 key/value heads, 21 rows (32 computed):
+//   74 x  512 keys [8]    29 / 33     27 / 35     22 / 22
+//   74 x 1024 keys [16]   41 / 47     37 / 47     33 / 25
+// and with scores, where a CTA also goes through its keys' logits on its own
+// (all full, one full):
+//   16 x 1536 keys [12]   33 / 33     25 / 27
+//   32 x 1024 keys [16]   37 / 39     29 / 22
+// So a skewed batch loses a few us at most. The host saves another 2 us.
 constexpr int kClusterMore = 4;
-void plan_cluster(AttnPlan* p, int keys) {
+constexpr int kClusterTiles = 20, kClusterTilesScored = 12;
+void plan_cluster(AttnPlan* p, int keys, bool scored) {
   if (p->blocks != 1 || p->block > 32 || p->units > 2 * kSms) return;
   const int tiles = (keys + 63) / 64;
   int cs = 1;
   while (cs < 8 && 2 * cs * p->units <= 2 * kSms && 2 * cs <= tiles) cs *= 2;
   const int mine = (tiles + cs - 1) / cs, flat = (int)(((int64_t)p->units * tiles + 2 * kSms - 1) / (2 * kSms));
-  if (mine > flat + kClusterMore) return;
+  if (mine > flat + kClusterMore || mine * (p->block / 16) > (scored ? kClusterTilesScored : kClusterTiles)) return;
   p->cluster = cs;
   p->slots = 0;
 }
@@ -252,7 +267,7 @@ CachePlan plan_cache(const CacheShape& s, int op) {
     };
     const int most_rows = s.fp32 ? 32 : 64;
     p.main = plan(units, rows, keys, s.fp32 ? rows <= most_rows : s.n_q <= kMaxDraft, false);
-    if (p.main.kernel == kDecodeMma && !p.has_pre) plan_cluster(&p.main, keys);
+    if (p.main.kernel == kDecodeMma && !p.has_pre) plan_cluster(&p.main, keys, op == CRISP_CACHE_SCORED);
     if (p.has_pre) p.pre = plan(s.h_kv, s.batch * rows, s.n_prefix, s.batch * rows <= most_rows, true);
     // output rows straight away when no row's keys are split
     if (op == CRISP_CACHE_WINDOW && !decodes(p.main) && p.main.splits == 1) p.main.slots = 0;

@@ -24,7 +24,8 @@
 // reads in its second launch.
 //
 // Small calls (CL): a cluster of 1 to 8 CTAs has a job to itself, each CTA a
-// part of its key tiles; they join their results through distributed shared
+// part of its key tiles (at most 20, so that one long sequence among short
+// ones, which the flat list would deal to every SM, costs little); they join their results through distributed shared
 // memory, write the output rows and add the scores of their own keys, in one
 // launch (about 3 us on the GPU and 2 on the host less than two).
 //

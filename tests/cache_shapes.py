@@ -19,3 +19,7 @@ TWO_TILES = [
     # a window that has just left the first keys behind; first keys that reach into it
     ((1, 32, 8, 1000, 2600, [2599], 1900, 700), False),
 ]
+
+# Decode, bf16, with one full sequence among short ones, on the flat list of key
+# tiles: (b, hq, hkv, nq, nk)
+SKEWED = [(37, 32, 8, 1, 2500), (74, 28, 4, 3, 900), (33, 8, 1, 2, 12000)]

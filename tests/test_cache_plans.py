@@ -70,3 +70,27 @@ def test_long_key_lists_take_two_row_tiles(plan, case, split):
 def test_two_row_tile_shapes_include_a_cta_without_a_second_one(plan):
     odd = [plan(crisp.CACHE_WINDOW, *c[:5], c[6], c[7])["row_tiles"] % 2 for c, _ in shapes.TWO_TILES]
     assert 0 in odd and 1 in odd
+
+
+@pytest.mark.parametrize("op", [crisp.CACHE_WINDOW, crisp.CACHE_SCORED])
+def test_a_cluster_never_walks_a_long_list_alone(plan, op):
+    """Lengths are unknown to the plan: in a batch of one full sequence and many short ones a cluster's CTAs walk the
+    full one alone, so their share has to stay small whatever the flat list's share of a full batch would be."""
+    took = 0
+    for b, hq, hkv, nq in ((1, 32, 8, 1), (8, 32, 8, 1), (36, 32, 8, 1), (37, 32, 8, 1), (74, 28, 4, 3), (148, 32, 2, 1),
+                           (296, 8, 1, 2), (37, 32, 8, 7)):
+        for nk in (512, 1024, 2048, 4096, 9472, 131072):
+            p = plan(op, b, hq, hkv, nq, nk)
+            if p["cluster"] == 0:
+                continue
+            took += 1
+            share = -(-(-(-nk // 64)) // p["cluster"]) * (p["block"] // 16)
+            assert share <= (12 if op == crisp.CACHE_SCORED else 20), (b, hq, hkv, nq, nk, p)
+    assert took > 8
+    for case in shapes.SKEWED:
+        assert plan(op, *case)["cluster"] == 0
+    # short caches and windows keep their one launch
+    assert plan(op, 1, 32, 8, 1, 512)["cluster"] == 8
+    assert plan(op, 37, 32, 8, 1, 512)["cluster"] == 1
+    if op == crisp.CACHE_WINDOW:
+        assert plan(op, 32, 32, 8, 1, 8192, 1024, 4)["cluster"] == 1

@@ -43,3 +43,20 @@ def test_token_major_layout_with_two_row_tiles():
     assert crisp.cache_device_status(cfg) == 0
     check()
     close(out, *plain.attention(q, k, v, [nk] * b, 1850, 33)[:2])
+
+
+@pytest.mark.parametrize("case", shapes.SKEWED, ids=lambda c: "-".join(map(str, c)))
+def test_one_long_sequence_among_short_ones(case):
+    b, hq, hkv, nq, nk = case
+    lens = [(7 * s) % 60 for s in range(b)]
+    lens[b // 2] = nk
+    q, k, v, kv_len, cfg = make("bf16", b, hq, hkv, nq, nk, lens, seed=32)
+    out = run_window(q, k, v, kv_len, cfg)
+    want, tol, add, add_tol = plain.attention(q, k, v, lens)
+    close(out, want, tol)
+    cfg.allocate_workspace(crisp.CACHE_SCORED)
+    score = torch.zeros(b, hkv, nk, device="cuda")
+    crisp.scored_attention(q, k, v, out, score, cfg, kv_len=kv_len)
+    assert crisp.cache_device_status(cfg) == 0
+    close(out, want, tol)
+    close(score, add, add_tol + plain.U * add)
