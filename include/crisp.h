@@ -325,9 +325,11 @@ crisp_status crisp_evict(const void* k, const void* v, const float* score, const
                          void* v_new, float* score_new, int32_t* kept, int32_t* new_len,
                          const crisp_cache_cfg* cfg, void* stream);
 
-/* Synchronise `stream`, then read (and clear) what the last cache operator
- * that used cfg->workspace reported: CRISP_OK, CRISP_ERR_TIMEOUT, or
- * CRISP_ERR_INVALID_ARG for a kv_len that was clamped. */
+/* Read (and clear) what the last cache operator that used cfg->workspace
+ * reported: CRISP_OK, CRISP_ERR_TIMEOUT, or CRISP_ERR_INVALID_ARG for a kv_len
+ * that was clamped. Works on `stream`, behind what was enqueued there before
+ * and ahead of what comes after, and synchronises it. The workspace's device
+ * has to be the current one. */
 crisp_status crisp_cache_device_status(const crisp_cache_cfg* cfg, void* stream, int32_t* device_status);
 
 /* Diagnostics: evaluate, on the device, the exp2 approximations the kernels

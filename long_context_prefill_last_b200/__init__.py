@@ -562,8 +562,16 @@ def evict(k, v, score, k_new, v_new, score_new, kept, new_len, cfg: CacheConfig,
 
 
 def cache_device_status(cfg: CacheConfig, stream=None) -> int:
-    """Synchronise the stream and return (and clear) what the last cache operator on cfg.workspace reported."""
+    """Return (and clear) what the last cache operator on cfg.workspace reported, after synchronising `stream`
+    (default: the current stream of the workspace's device, which is made current)."""
     st = ctypes.c_int32(0)
-    _check(lib().crisp_cache_device_status(ctypes.byref(cfg._c()), _stream(stream), ctypes.byref(st)),
-           "crisp_cache_device_status")
+    index = None if cfg.workspace is None else cfg.workspace.get_device()
+    if index is None:       # refused by the library
+        code = lib().crisp_cache_device_status(ctypes.byref(cfg._c()), None, ctypes.byref(st))
+    elif index < 0:
+        raise ValueError(f"the workspace is on {cfg.workspace.device}; the cache operators take CUDA tensors")
+    else:
+        with _torch_module().cuda.device(index):
+            code = lib().crisp_cache_device_status(ctypes.byref(cfg._c()), _stream(stream), ctypes.byref(st))
+    _check(code, "crisp_cache_device_status")
     return st.value

@@ -541,9 +541,11 @@ crisp_status crisp_cache_device_status(const crisp_cache_cfg* cfg, void* stream,
   if (r != CRISP_OK) return r;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int32_t word[8] = {0};
+  // all on `st`: the default stream would wait for other streams' work, and what
+  // follows on `st` would not wait for its clearing
+  CACHE_TRY(cudaMemcpyAsync(word, cfg->workspace, sizeof(word), cudaMemcpyDeviceToHost, st));
+  CACHE_TRY(cudaMemsetAsync(cfg->workspace, 0, sizeof(word), st));
   CACHE_TRY(cudaStreamSynchronize(st));
-  CACHE_TRY(cudaMemcpy(word, cfg->workspace, sizeof(word), cudaMemcpyDeviceToHost));
-  CACHE_TRY(cudaMemset(cfg->workspace, 0, sizeof(word)));
   *device_status = word[kStatusCode] != 0 ? word[kStatusCode] : word[kStatusLen];
   return CRISP_OK;
 }

@@ -60,3 +60,24 @@ def test_one_long_sequence_among_short_ones(case):
     assert crisp.cache_device_status(cfg) == 0
     close(out, want, tol)
     close(score, add, add_tol + plain.U * add)
+
+
+def test_device_status_works_on_its_stream():
+    """Reading and clearing the status waits for its own stream only, so that what follows there comes after it."""
+    q, k, v, _, cfg = make("bf16", 1, 4, 2, 1, 64, [64])
+    cfg.allocate_workspace(crisp.CACHE_WINDOW)
+    lens = torch.tensor([65], dtype=torch.int32, device="cuda")
+    out = torch.empty_like(q)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(2):      # the first call loads the kernels
+        crisp.window_attention(q, k, v, out, cfg, kv_len=lens, stream=side)
+        assert crisp.cache_device_status(cfg, side) == 1
+    crisp.window_attention(q, k, v, out, cfg, kv_len=lens, stream=side)
+    torch.cuda._sleep(1_000_000_000)        # half a second on the current stream
+    busy = torch.cuda.Event()
+    busy.record()
+    assert crisp.cache_device_status(cfg, side) == 1
+    assert crisp.cache_device_status(cfg, side) == 0
+    assert not busy.query()
+    torch.cuda.synchronize()
