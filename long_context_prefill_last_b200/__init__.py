@@ -413,10 +413,15 @@ class CacheConfig:
     workspace: Optional[object] = None     # torch.uint8 CUDA tensor
     reserved: int = 0
 
+    _kept = None     # the C structure of the last call, (strides, names, reference)
+
     def __setattr__(self, name, value):
         # the C structure is kept between calls; any change makes a new one
         self.__dict__[name] = value
-        self.__dict__["_kept"] = None
+        self.__dict__.pop("_kept", None)
+
+    def __getstate__(self):      # copies and pickles make their own C structure
+        return {name: x for name, x in self.__dict__.items() if name != "_kept"}
 
     def _c(self, **tensors) -> _CacheCfg:
         """A C structure for these tensors' strides."""
@@ -444,9 +449,9 @@ class CacheConfig:
         kept = self._kept
         if kept is not None and kept[0] == strides and kept[1] is names:
             return kept[2]
-        c = self._c(**dict(zip(names, tensors)))
-        self.__dict__["_kept"] = (strides, names, ctypes.byref(c))
-        return self._kept[2]
+        ref = ctypes.byref(self._c(**dict(zip(names, tensors))))
+        self.__dict__["_kept"] = (strides, names, ref)
+        return ref      # not what is kept: another thread's call may have replaced it
 
     def allocate_workspace(self, op: int, device="cuda"):
         """Device workspace for operator `op` (CACHE_WINDOW, CACHE_SCORED, CACHE_PREFIX, CACHE_EVICT); the

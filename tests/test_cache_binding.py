@@ -1,6 +1,10 @@
 """The cache operators' binding: devices, copies and concurrent use of a
 configuration (no GPU needed)."""
 import contextlib
+import copy
+import dataclasses
+import pickle
+import sys
 
 import pytest
 
@@ -67,3 +71,48 @@ def test_device_status_without_a_device_workspace_is_refused():
     cfg.workspace = torch.zeros(256, dtype=torch.uint8)
     with pytest.raises(ValueError, match="CUDA"):
         crisp.cache_device_status(cfg)
+
+
+NAMES = ("k",)
+
+
+def used():
+    cfg = crisp.CacheConfig(batch=1, n_q=1, n_k=16, h_q=2, h_kv=2, window=5)
+    cfg._ref(NAMES, [torch.zeros(1, 2, 16, 128)])
+    return cfg
+
+
+@pytest.mark.parametrize("make", [copy.copy, copy.deepcopy, lambda c: pickle.loads(pickle.dumps(c)),
+                                  dataclasses.replace], ids=["copy", "deepcopy", "pickle", "replace"])
+def test_a_used_configuration_can_be_copied(make):
+    cfg = used()
+    other = make(cfg)
+    assert other == cfg and other.window == 5
+    t = [torch.zeros(1, 2, 16, 128)]
+    ref = cfg._ref(NAMES, t)
+    assert other._ref(NAMES, t)._obj is not ref._obj
+    other.window = 9
+    assert other._ref(NAMES, t)._obj.window == 9 and cfg._ref(NAMES, t) is ref and ref._obj.window == 5
+
+
+def test_two_threads_calls_get_their_own_structures():
+    """Another call on the same configuration, between any two lines of this one."""
+    dense, sparse = [torch.zeros(1, 2, 16, 128)], [torch.zeros(1, 16, 2, 128).transpose(1, 2)]
+    cfg = used()
+    cfg.window = 6
+
+    def interrupt(frame, event, arg):
+        if frame.f_code.co_name != "_ref":
+            return None
+        if event == "line":
+            sys.settrace(None)
+            cfg._ref(NAMES, sparse)
+            sys.settrace(interrupt)
+        return interrupt
+
+    sys.settrace(interrupt)
+    try:
+        ref = cfg._ref(NAMES, dense)
+    finally:
+        sys.settrace(None)
+    assert ref._obj.k.head == dense[0].stride(1)
