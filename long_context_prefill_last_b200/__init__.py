@@ -413,7 +413,7 @@ class CacheConfig:
     workspace: Optional[object] = None     # torch.uint8 CUDA tensor
     reserved: int = 0
 
-    _kept = None     # the C structure of the last call, (strides, names, reference)
+    _kept = None     # the C structure of the last call: (strides and workspace, names, reference)
 
     def __setattr__(self, name, value):
         # the C structure is kept between calls; any change makes a new one
@@ -444,8 +444,10 @@ class CacheConfig:
         return c
 
     def _ref(self, names, tensors):
-        """A reference to the C structure for these tensors; the last one is kept while nothing changes."""
-        strides = [t.stride() for t in tensors]
+        """A reference to the C structure for these tensors; the last one is kept while nothing changes (a workspace
+        resized in place included)."""
+        ws = self.workspace
+        strides = [t.stride() for t in tensors] + [None if ws is None else (ws.data_ptr(), ws.numel())]
         kept = self._kept
         if kept is not None and kept[0] == strides and kept[1] is names:
             return kept[2]

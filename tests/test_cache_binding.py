@@ -116,3 +116,13 @@ def test_two_threads_calls_get_their_own_structures():
     finally:
         sys.settrace(None)
     assert ref._obj.k.head == dense[0].stride(1)
+
+
+def test_a_workspace_resized_in_place_is_noticed():
+    cfg = crisp.CacheConfig(batch=1, n_q=1, n_k=16, h_q=2, h_kv=2)
+    cfg.workspace = torch.zeros(256, dtype=torch.uint8)
+    t = [torch.zeros(1, 2, 16, 128)]
+    assert cfg._ref(NAMES, t)._obj.workspace_bytes == 256
+    cfg.workspace.resize_(1 << 20)
+    c = cfg._ref(NAMES, t)._obj
+    assert c.workspace == cfg.workspace.data_ptr() and c.workspace_bytes == 1 << 20
