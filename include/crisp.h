@@ -317,10 +317,11 @@ crisp_status crisp_shared_prefix_attention(const void* q, const void* k_prefix, 
  * slots 0 .. new_len[b] - 1 of k_new, v_new and score_new (float32, contiguous
  * [batch][h_kv][n_new]); later scores become 0, later keys and values are left
  * as they were. kept (int32 [batch][h_kv][budget]) gets the old indices,
- * ascending, then -1; new_len (int32 [batch], not kv_len itself) the lengths.
- * The new cache must not overlap the old one; the address ranges from their
- * first to their last element are compared (CRISP_ERR_INVALID_ARG). n_q, window
- * and sm_scale are not used. */
+ * ascending, then -1; new_len (int32 [batch]) the lengths. No output may
+ * overlap an input (new_len is not kv_len), and score_new, kept and new_len no
+ * other output; the address ranges from first to last element are compared
+ * (CRISP_ERR_INVALID_ARG). k_new and v_new may lie interleaved in one buffer.
+ * n_q, window and sm_scale are not used. */
 crisp_status crisp_evict(const void* k, const void* v, const float* score, const int32_t* kv_len, void* k_new,
                          void* v_new, float* score_new, int32_t* kept, int32_t* new_len,
                          const crisp_cache_cfg* cfg, void* stream);

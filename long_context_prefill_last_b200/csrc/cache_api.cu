@@ -111,14 +111,17 @@ crisp_status check_workspace(const crisp_cache_cfg* c, size_t need) {
   return c->workspace_bytes < need ? CRISP_ERR_WORKSPACE : CRISP_OK;
 }
 
-// Whether the byte ranges of two strided tensors meet.
-bool ranges_meet(const void* a, const Strides& sa, int na, const void* b, const Strides& sb, int nb, const CacheShape& s) {
-  const int e = s.fp32 ? 4 : 2;
-  auto bytes = [&](const Strides& t, int n) {
-    return ((s.batch - 1) * t.seq + (s.h_kv - 1) * t.head + (int64_t)(n - 1) * t.token + kHeadDim) * e;
-  };
-  const char *pa = static_cast<const char*>(a), *pb = static_cast<const char*>(b);
-  return pa < pb + bytes(sb, nb) && pb < pa + bytes(sa, na);
+// The bytes from a tensor's first to its last element.
+struct Range {
+  const char *from, *to;
+  bool meets(const Range& o) const { return from < o.to && o.from < to; }
+};
+Range cache_range(const void* p, const Strides& t, int tokens, const CacheShape& s) {
+  const int64_t elems = (s.batch - 1) * t.seq + (s.h_kv - 1) * t.head + (int64_t)(tokens - 1) * t.token + kHeadDim;
+  return Range{static_cast<const char*>(p), static_cast<const char*>(p) + elems * (s.fp32 ? 4 : 2)};
+}
+Range word_range(const void* p, int64_t n) {   // NULL: empty
+  return Range{static_cast<const char*>(p), static_cast<const char*>(p) + (p == nullptr ? 0 : n * 4)};
 }
 
 // How many CTAs share a job's key tiles. Splitting shortens the longest CTA but
@@ -499,13 +502,20 @@ crisp_status crisp_evict(const void* k, const void* v, const float* score, const
   for (const void* w : words)
     if ((r = check_words(w, false)) != CRISP_OK) return r;
   if ((r = check_words(kv_len, true)) != CRISP_OK) return r;
-  if (kv_len == new_len) return CRISP_ERR_INVALID_ARG;
-  for (int i = 0; i < 2; ++i)
-    for (int j = 2; j < 4; ++j)
-      if (ranges_meet(t[i], i == 0 ? s.k : s.v, s.n_k, t[j], j == 2 ? s.k_new : s.v_new, s.n_new, s))
-        return CRISP_ERR_INVALID_ARG;
+  // nothing that is written may be an input, or another output; k_new and v_new may lie interleaved
   const int64_t units = (int64_t)s.batch * s.h_kv;
-  if (score < score_new + units * s.n_new && score_new < score + units * s.n_k) return CRISP_ERR_INVALID_ARG;
+  const Range in[] = {cache_range(k, s.k, s.n_k, s), cache_range(v, s.v, s.n_k, s), word_range(score, units * s.n_k),
+                      word_range(kv_len, s.batch)};
+  const Range out[] = {cache_range(k_new, s.k_new, s.n_new, s), cache_range(v_new, s.v_new, s.n_new, s),
+                       word_range(score_new, units * s.n_new), word_range(kept, units * s.budget),
+                       word_range(new_len, s.batch)};
+  if (k_new == v_new) return CRISP_ERR_INVALID_ARG;
+  for (int i = 0; i < 5; ++i) {
+    for (const Range& x : in)
+      if (out[i].meets(x)) return CRISP_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (i > 1 && out[i].meets(out[j])) return CRISP_ERR_INVALID_ARG;
+  }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   char* ws = static_cast<char*>(cfg->workspace);
   EvictArgs a{};
