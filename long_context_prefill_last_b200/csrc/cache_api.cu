@@ -259,17 +259,23 @@ CachePlan plan_cache(const CacheShape& s, int op) {
     const int keys = (int)std::min<int64_t>(s.n_k, seen);
     p.has_pre = op == CRISP_CACHE_PREFIX;
     // Few rows (a draft's, or those of all sequences for the prefix) take a
-    // decode kernel, more a tile kernel: in bf16 up to 64 rows, where the
-    // legacy tensor instruction still keeps up with memory, in fp32 up to 32,
-    // where two passes of 16 rows over the keys (80 cycles a key) beat the 64-row
-    // tile (128).
+    // decode kernel, more a tile kernel. In bf16 up to 64 rows (of 16 tokens),
+    // where the legacy tensor instruction still keeps up with memory and one job
+    // holds them all (a second row block would read every key again); in fp32 up
+    // to 32, where two passes of 16 rows over the keys (80 cycles a key) beat the
+    // 64-row tile (128). Scores in bf16 need the decode kernel's logits.
+    // Measured on bf16 drafts (decode kernel / tcgen05 kernel, us): 70 rows of 7
+    // heads a group, 1 x 4096 keys 22 / 18, 1 x 65536 86 / 45, 8 x 8192 86 / 45, 64
+    // x 600 76 / 29; 256 rows of 16 heads, 1 x 65536 57 / 31, 64 x 600 51 / 20. A
+    // window of 512 keys of one sequence is the other way round, 14 / 18.
     auto plan = [&](int n_units, int n_rows, int n_keys, bool few, bool prefix) {
       return few      ? plan_decode(n_units, n_rows, n_keys, s.fp32)
              : s.fp32 ? plan_tile(n_units, n_rows, n_keys)
                       : plan_tc(n_units, s.group, s.n_q, s.batch, prefix, n_keys);
     };
     const int most_rows = s.fp32 ? 32 : 64;
-    p.main = plan(units, rows, keys, s.fp32 ? rows <= most_rows : s.n_q <= kMaxDraft, false);
+    const bool few = rows <= most_rows && (s.fp32 || s.n_q <= kMaxDraft);
+    p.main = plan(units, rows, keys, few || (!s.fp32 && op == CRISP_CACHE_SCORED), false);
     if (p.main.kernel == kDecodeMma && !p.has_pre) plan_cluster(&p.main, keys, op == CRISP_CACHE_SCORED);
     if (p.has_pre) p.pre = plan(s.h_kv, s.batch * rows, s.n_prefix, s.batch * rows <= most_rows, true);
     // output rows straight away when no row's keys are split

@@ -23,3 +23,12 @@ TWO_TILES = [
 # Decode, bf16, with one full sequence among short ones, on the flat list of key
 # tiles: (b, hq, hkv, nq, nk)
 SKEWED = [(37, 32, 8, 1, 2500), (74, 28, 4, 3, 900), (33, 8, 1, 2, 12000)]
+
+# Drafts of up to 16 tokens with more rows than one decode job holds, bf16:
+# (b, hq, hkv, nq, nk, lens, window, sinks)
+WIDE_DRAFTS = [
+    (2, 28, 4, 16, 5000, [5000, 3], 0, 0),
+    (3, 16, 1, 5, 700, [700, 0, 4], 100, 7),
+    (2, 32, 2, 16, 2600, [2600, 1201], 1900, 130),
+    (9, 28, 4, 10, 300, [300, 10, 9, 0, 1, 299, 150, 64, 65], 0, 0),
+]

@@ -94,3 +94,20 @@ def test_a_cluster_never_walks_a_long_list_alone(plan, op):
     assert plan(op, 37, 32, 8, 1, 512)["cluster"] == 1
     if op == crisp.CACHE_WINDOW:
         assert plan(op, 32, 32, 8, 1, 8192, 1024, 4)["cluster"] == 1
+
+
+def test_drafts_that_one_job_cannot_hold_read_their_keys_once(plan):
+    """Above 64 rows the decode kernel would read every key once per 64 rows; only scores need it."""
+    for c in shapes.WIDE_DRAFTS:
+        b, hq, hkv, nq, nk, _, window, sinks = c
+        assert nq * hq // hkv > 64
+        assert plan(crisp.CACHE_WINDOW, b, hq, hkv, nq, nk, window, sinks)["kernel"] == TILE_TC
+        assert plan(crisp.CACHE_PREFIX, b, hq, hkv, nq, nk, n_prefix=500)["kernel"] == TILE_TC
+        assert plan(crisp.CACHE_SCORED, b, hq, hkv, nq, nk, window, sinks)["kernel"] == DECODE_MMA
+    for op in (crisp.CACHE_WINDOW, crisp.CACHE_PREFIX):
+        assert plan(op, 2, 28, 4, 9, 5000, n_prefix=500)["kernel"] == DECODE_MMA     # 63 rows
+        assert plan(op, 2, 32, 8, 16, 5000, n_prefix=500)["kernel"] == DECODE_MMA    # 64
+        assert plan(op, 2, 28, 4, 10, 5000, n_prefix=500)["kernel"] == TILE_TC       # 70
+    assert plan(crisp.CACHE_WINDOW, 2, 4, 4, 17, 5000)["kernel"] == TILE_TC           # a prompt
+    assert plan(crisp.CACHE_WINDOW, 2, 4, 4, 17, 5000, fp32=1)["kernel"] == DECODE_SIMT
+    assert plan(crisp.CACHE_SCORED, 2, 28, 4, 16, 5000, fp32=1)["kernel"] == SIMT_TILE

@@ -81,3 +81,31 @@ def test_device_status_works_on_its_stream():
     assert crisp.cache_device_status(cfg, side) == 0
     assert not busy.query()
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("case", shapes.WIDE_DRAFTS, ids=lambda c: "-".join(map(str, c)).replace(" ", ""))
+def test_drafts_of_many_rows(case, dtype):
+    """Through a window, with scores, and behind a shared prefix."""
+    b, hq, hkv, nq, nk, lens, window, sinks = case
+    q, k, v, kv_len, cfg = make(dtype, b, hq, hkv, nq, nk, lens, seed=33, window=window, sinks=sinks)
+    out = run_window(q, k, v, kv_len, cfg)
+    want, tol, add, add_tol = plain.attention(q, k, v, lens, window, sinks)
+    close(out, want, tol)
+    score, check = guarded(b, hkv, nk, dtype=torch.float32, fill=0.0)
+    cfg.allocate_workspace(crisp.CACHE_SCORED)
+    crisp.scored_attention(q, k, v, out, score, cfg, kv_len=kv_len)
+    assert crisp.cache_device_status(cfg) == 0
+    check()
+    close(out, want, tol)
+    close(score, add, add_tol + plain.U * add)
+    gen = torch.Generator("cuda").manual_seed(34)
+    for npre in (1, 500, 2500):
+        q, k, v, kv_len, cfg = make(dtype, b, hq, hkv, nq, nk, lens, seed=35, n_prefix=npre)
+        kp, vp = (randn(gen, hkv, npre, D, dtype=q.dtype) for _ in range(2))
+        out, check = guarded(*q.shape, dtype=q.dtype)
+        cfg.allocate_workspace(crisp.CACHE_PREFIX)
+        crisp.shared_prefix_attention(q, kp, vp, k, v, out, cfg, kv_len=kv_len)
+        assert crisp.cache_device_status(cfg) == 0
+        check()
+        close(out, *plain.attention(q, k, v, lens, k_prefix=kp, v_prefix=vp)[:2])
