@@ -332,6 +332,7 @@ struct AttnPlan {
   int block, blocks, splits, ctas, tile;
   int slot_rows;     // rows of a partial slot: the block's, or the unit's where it has only one block
   int tok_box, seq_box, row_tiles;   // kTileTc
+  int run;           // kTileSimt: key tiles of a CTA, at most
   int units;
   int cluster;       // kDecodeMma: CTAs per job that join their results themselves (0: see kStair)
   size_t slots;      // partial slots (0: the kernel writes the output itself)

@@ -155,6 +155,7 @@ AttnPlan plan_tile(int units, int rows, int keys) {
   p.blocks = (rows + 63) / 64;
   const int64_t jobs = (int64_t)units * p.blocks;
   p.splits = plan_splits(jobs, (keys + 63) / 64, (int64_t)units * rows, 2 * kSms, 4.5);
+  p.run = ((keys + 63) / 64 + p.splits - 1) / p.splits;
   p.slots = (size_t)jobs * p.splits;
   return p;
 }

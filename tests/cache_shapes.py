@@ -32,3 +32,7 @@ WIDE_DRAFTS = [
     (2, 32, 2, 16, 2600, [2600, 1201], 1900, 130),
     (9, 28, 4, 10, 300, [300, 10, 9, 0, 1, 299, 150, 64, 65], 0, 0),
 ]
+
+# fp32 calls whose CTAs take many key tiles each: (b, hq, hkv, nq, nk), key tiles of a CTA
+LONG_RUNS_DECODE = ((37, 8, 8, 1, 131072), 4096)       # cache_decode_fp32.cu, 32 keys a tile
+LONG_RUNS_TILE = ((150, 12, 1, 3, 131072), 2048)       # cache_tile.cu, 64 keys a tile

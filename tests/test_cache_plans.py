@@ -111,3 +111,12 @@ def test_drafts_that_one_job_cannot_hold_read_their_keys_once(plan):
     assert plan(crisp.CACHE_WINDOW, 2, 4, 4, 17, 5000)["kernel"] == TILE_TC           # a prompt
     assert plan(crisp.CACHE_WINDOW, 2, 4, 4, 17, 5000, fp32=1)["kernel"] == DECODE_SIMT
     assert plan(crisp.CACHE_SCORED, 2, 28, 4, 16, 5000, fp32=1)["kernel"] == SIMT_TILE
+
+
+def test_fp32_long_runs(plan):
+    (b, hq, hkv, nq, nk), tiles = shapes.LONG_RUNS_DECODE
+    p = plan(crisp.CACHE_SCORED, b, hq, hkv, nq, nk, fp32=1)
+    assert p["kernel"] == DECODE_SIMT and b * hkv * p["blocks"] * (nk // 32) == tiles * p["ctas"]
+    (b, hq, hkv, nq, nk), tiles = shapes.LONG_RUNS_TILE
+    p = plan(crisp.CACHE_SCORED, b, hq, hkv, nq, nk, fp32=1)
+    assert p["kernel"] == SIMT_TILE and p["splits"] == 1 and nk // 64 == tiles

@@ -1,6 +1,8 @@
 """Paths of the cache operators that single out a kernel form, on the GPU
 against the definitions in 64 bits (tests/cache_plain.py derives the
 tolerances; tests/test_cache_plans.py checks that the shapes take the path)."""
+import math
+
 import pytest
 
 import cache_plain as plain
@@ -109,3 +111,61 @@ def test_drafts_of_many_rows(case, dtype):
         assert crisp.cache_device_status(cfg) == 0
         check()
         close(out, *plain.attention(q, k, v, lens, k_prefix=kp, v_prefix=vp)[:2])
+
+
+@pytest.mark.parametrize("path,delta,held", [("decode", 1.2, 0), ("tile", 1.7, 64)])
+def test_long_fp32_sums_of_like_weights(path, delta, held):
+    """Keys that all weigh 2^-delta of a few first ones: a CTA's sums run over thousands of equal tiles, where the
+    roundings of a plain running sum fall to one side (off by 4e-5 and 3e-5 here).
+
+    Bounds, from u = 2^-24 and the arithmetic alone. q and k have one dimension that is not zero, so a logit is one
+    product (u), scaled (u, and 2 u for the scale itself), subtracted (u) and of a key rounded to fp32 (u): off by 6 u of
+    the larger logit in base 2, which a weight's relative error stays below. An exponential is off by 2^-21 at most.
+    The denominator: 8 additions inside a tile, then a compensated sum (2 u) or `held` tiles at a time (held + tiles /
+    held), then 4 pieces. A score: two exponentials' errors, the denominator's, up to 36 rows added. An output: every
+    value is the same, so the weights' errors cancel; a chain of 64 inside a tile and over tiles as before, twice."""
+    (b, hq, hkv, nq, nk), tiles = shapes.LONG_RUNS_DECODE if path == "decode" else shapes.LONG_RUNS_TILE
+    first = 200
+    # sequence s, head h: the same keys from token s + h on, with 50 heavy keys or more in front
+    gen = torch.Generator("cuda").manual_seed(36)
+    keys = torch.zeros(nk + first, D, device="cuda")
+    x = 2.5
+    keys[:first, 5] = x
+    keys[first:, 5] = x - delta
+    values = torch.randn(D, generator=gen, device="cuda").expand(nk + first, D).contiguous()
+    step = 128
+    k, v = (t.as_strided((b, hkv, nk, D), (step, step, D, 1)) for t in (keys, values))
+    q = torch.zeros(b, hq, nq, D, device="cuda")
+    q[..., 5] = 1.0
+    cfg = crisp.CacheConfig(batch=b, n_q=nq, n_k=nk, h_q=hq, h_kv=hkv, dtype=crisp.FP32, sm_scale=math.log(2))
+    cfg.allocate_workspace(crisp.CACHE_SCORED)
+    out, score = torch.empty_like(q), torch.zeros(b, hkv, nk, device="cuda")
+    crisp.scored_attention(q, k, v, out, score, cfg)
+    assert crisp.cache_device_status(cfg) == 0
+    u = plain.U
+    over = (held + tiles / held if held else 2) + 4
+    rel_score = 2 * (6 * u * x + 2.0 ** -21) + (8 + over + 36) * u
+    rel_out = (8 + 64 + 2 * over) * u
+    for s, h in ((0, 0), (b - 1, hkv - 1), (b // 2, 0)):
+        heavy = first - s - h
+        w = torch.full((nk,), 2.0 ** -delta, dtype=torch.float64, device="cuda")
+        w[:heavy] = 1.0
+        place = nk - nq + torch.arange(nq, device="cuda")[:, None]
+        p = torch.where(torch.arange(nk, device="cuda") <= place, w, torch.zeros_like(w))
+        p = p / p.sum(1, keepdim=True)
+        want = p.sum(0) * (hq // hkv)
+        close(score[s, h], want, want * rel_score)
+        want = values[0].double().expand(hq // hkv, nq, D)
+        close(out[s, h * (hq // hkv):(h + 1) * (hq // hkv)], want, want.abs() * rel_out)
+
+
+@pytest.mark.parametrize("case", [(1, 2, 2, 5000, 5000, [5000], 0, 0), (2, 4, 4, 2500, 14000, [14000, 9000], 0, 3),
+                                  (2, 48, 16, 3, 9000, [9000, 8998], 0, 0)],
+                         ids=lambda c: "-".join(map(str, c)).replace(" ", ""))
+def test_fp32_prompts_of_more_tiles_than_registers_hold(case):
+    b, hq, hkv, nq, nk, lens, window, sinks = case
+    q, k, v, kv_len, cfg = make("fp32", b, hq, hkv, nq, nk, lens, seed=37, sharp=2.0, window=window, sinks=sinks)
+    want, tol, _, _ = plain.attention(q, k, v, lens, window, sinks)
+    out = run_window(q, k, v, kv_len, cfg)
+    close(out, want, tol)
+    assert torch.equal(out, run_window(q, k, v, kv_len, cfg))
