@@ -13,7 +13,7 @@ namespace crisp {
 
 constexpr int kMaxBatch = 1024;          // sequences of one call
 constexpr int kMaxCacheLen = 1 << 24;    // key slots per sequence
-constexpr int kMaxDraft = 16;            // query tokens of a scored or shared-prefix call, and of the decode kernels
+constexpr int kMaxDraft = 16;            // query tokens of a scored or shared-prefix call, and of the bf16 decode kernel
 constexpr int kNoWindow = 1 << 30;       // window = 0: every earlier key
 constexpr int kStatusLen = 4;            // status slot: a sequence length outside [0, n_k] (it was clamped)
 
@@ -63,16 +63,10 @@ inline KeyList key_list(int len, int n_q, int i0, int i1, int window, int sinks)
   return r;
 }
 
-// How the rows of one attention launch are laid out. A unit is one key/value
-// head of one sequence; its rows are its (token, head of the group) pairs,
-// token-major. For the shared prefix a unit is one key/value head and its
-// rows are those of every sequence, one after another.
-struct RowMap {
-  int n_q, group, h_kv;
-  int rows;          // per unit
-  int per_seq;       // n_q * group
-  bool prefix;
-};
+// Units and rows of an attention launch: a unit is one key/value head of one
+// sequence; its rows are its (token, head of the group) pairs, token-major. For
+// the shared prefix a unit is one key/value head and its rows are those of
+// every sequence, one after another.
 
 // Where an attention launch leaves a row's partial results: runs of
 // consecutive slots of `block` rows each. kSplits: slot = job * splits + s.
@@ -391,7 +385,7 @@ inline cudaError_t launch_kernel(void (*kernel)(P...), unsigned grid, int thread
 struct FinishArgs {
   PartSrc main, pre;
   const int32_t* kv_len;
-  int batch, n_q, n_k, n_prefix, h_kv, group, window, sinks;
+  int batch, n_q, n_k, h_kv, group, window, sinks;
   void* out;
   Strides so;
   bool fp32;

@@ -404,7 +404,6 @@ crisp_status run_attention(const void* q, const void* kp, const void* vp, const 
   m.batch = s.batch;
   m.n_q = s.n_q;
   m.n_k = s.n_k;
-  m.n_prefix = s.n_prefix;
   m.h_kv = s.h_kv;
   m.group = s.group;
   m.window = s.window;
