@@ -413,7 +413,7 @@ class CacheConfig:
     workspace: Optional[object] = None     # torch.uint8 CUDA tensor
     reserved: int = 0
 
-    _kept = None     # the C structure of the last call: (strides and workspace, names, reference)
+    _kept = None     # the C structure of the last call: (strides, names, reference, workspace address)
 
     def __setattr__(self, name, value):
         # the C structure is kept between calls; any change makes a new one
@@ -447,12 +447,13 @@ class CacheConfig:
         """A reference to the C structure for these tensors; the last one is kept while nothing changes (a workspace
         resized in place included)."""
         ws = self.workspace
-        strides = [t.stride() for t in tensors] + [None if ws is None else (ws.data_ptr(), ws.numel())]
+        at = 0 if ws is None else ws.data_ptr()
+        strides = [t.stride() for t in tensors]
         kept = self._kept
-        if kept is not None and kept[0] == strides and kept[1] is names:
+        if kept is not None and kept[0] == strides and kept[1] is names and kept[3] == at:
             return kept[2]
         ref = ctypes.byref(self._c(**dict(zip(names, tensors))))
-        self.__dict__["_kept"] = (strides, names, ref)
+        self.__dict__["_kept"] = (strides, names, ref, at)
         return ref      # not what is kept: another thread's call may have replaced it
 
     def allocate_workspace(self, op: int, device="cuda"):
