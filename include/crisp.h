@@ -245,12 +245,20 @@ crisp_status crisp_route_noalloc(const void* q, const void* k, const crisp_cfg* 
  * key that some query of the sequence sees may reach every query of that
  * sequence. Query head h reads key/value head h / (h_q / h_kv).
  *
+ * Rounding: logits, softmax statistics, sums and scores are float32. The bf16
+ * operators round each softmax weight to bf16 before its product with v (the
+ * score of a key gets the float32 weight) and the result once more, so outputs
+ * are off by 2.0e-3 to 2.3e-3 (relative norm, weights spread over many keys)
+ * where the rounding of the result alone gives 1.7e-3. The fp32 operators
+ * round nothing to fewer bits. Results repeat to the bit.
+ *
  * The conventions above hold: arguments are checked before anything is
  * launched, nothing synchronises or allocates, and scratch lives in
  * cfg->workspace (256-byte aligned, >= crisp_cache_workspace_size bytes),
  * which calls that can overlap must not share: calls on one stream may, two
- * captured graphs only when they never run at the same time. The tensors'
- * device has to be the current one. A kv_len outside [0, n_k] is clamped
+ * captured graphs only when they never run at the same time. out may be q
+ * itself (address and strides); else out and score overlap no other tensor of
+ * the call. The tensors' device has to be the current one. A kv_len outside [0, n_k] is clamped
  * and reported by crisp_cache_device_status as CRISP_ERR_INVALID_ARG. */
 
 typedef struct {

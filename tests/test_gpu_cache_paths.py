@@ -169,3 +169,29 @@ def test_fp32_prompts_of_more_tiles_than_registers_hold(case):
     out = run_window(q, k, v, kv_len, cfg)
     close(out, want, tol)
     assert torch.equal(out, run_window(q, k, v, kv_len, cfg))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("case", [(3, 28, 4, 1, 500), (2, 8, 2, 16, 6000), (2, 28, 4, 16, 600), (1, 4, 2, 4500, 4500),
+                                  (1, 16, 1, 60, 5000), (37, 32, 8, 1, 2500)], ids=lambda c: "-".join(map(str, c)))
+def test_outputs_in_place_of_the_queries(case, dtype):
+    b, hq, hkv, nq, nk = case
+    q, k, v, lens, cfg = make(dtype, b, hq, hkv, nq, nk, [nk - 3 * s for s in range(b)], seed=38, n_prefix=900)
+    out, same = run_window(q, k, v, lens, cfg), q.clone()
+    crisp.window_attention(same, k, v, same, cfg, kv_len=lens)
+    assert torch.equal(out, same)
+    if nq > 16:
+        return
+    cfg.allocate_workspace(crisp.CACHE_SCORED)
+    scores = [torch.zeros(b, hkv, nk, device="cuda") for _ in range(2)]
+    same = q.clone()
+    crisp.scored_attention(q, k, v, out, scores[0], cfg, kv_len=lens)
+    crisp.scored_attention(same, k, v, same, scores[1], cfg, kv_len=lens)
+    assert torch.equal(out, same) and torch.equal(*scores)
+    gen = torch.Generator("cuda").manual_seed(39)
+    kp, vp = (randn(gen, hkv, 900, D, dtype=q.dtype) for _ in range(2))
+    cfg.allocate_workspace(crisp.CACHE_PREFIX)
+    same = q.clone()
+    crisp.shared_prefix_attention(q, kp, vp, k, v, out, cfg, kv_len=lens)
+    crisp.shared_prefix_attention(same, kp, vp, k, v, same, cfg, kv_len=lens)
+    assert torch.equal(out, same)
