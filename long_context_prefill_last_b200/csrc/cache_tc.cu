@@ -413,18 +413,17 @@ cache_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         ++u;
       }
     }
-    if (!ok) {
-      // error path: let the copies already issued land before the CTA exits
-      dev::mbar_drain(C::bar(sbase, C::b_q), 0);
-      if (hasB) dev::mbar_drain(C::bar(sbase, C::b_q + 1), 0);
-      for (int s = 0; s < C::k_stages && s < issued_k; ++s) {
-        const int last = issued_k - 1 - ((issued_k - 1 - s) % C::k_stages);
-        dev::mbar_drain(C::bar(sbase, C::b_kfull + s), (last / C::k_stages) & 1);
-      }
-      for (int s = 0; s < C::v_stages && s < issued_v; ++s) {
-        const int last = issued_v - 1 - ((issued_v - 1 - s) % C::v_stages);
-        dev::mbar_drain(C::bar(sbase, C::b_vfull + s), (last / C::v_stages) & 1);
-      }
+    // Every copy lands before the CTA exits: after an error (here or, reported
+    // through the status word, in another CTA) the others may not have waited for it
+    dev::mbar_drain(C::bar(sbase, C::b_q), 0);
+    if (hasB) dev::mbar_drain(C::bar(sbase, C::b_q + 1), 0);
+    for (int s = 0; s < C::k_stages && s < issued_k; ++s) {
+      const int last = issued_k - 1 - ((issued_k - 1 - s) % C::k_stages);
+      dev::mbar_drain(C::bar(sbase, C::b_kfull + s), (last / C::k_stages) & 1);
+    }
+    for (int s = 0; s < C::v_stages && s < issued_v; ++s) {
+      const int last = issued_v - 1 - ((issued_v - 1 - s) % C::v_stages);
+      dev::mbar_drain(C::bar(sbase, C::b_vfull + s), (last / C::v_stages) & 1);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
