@@ -258,8 +258,9 @@ crisp_status crisp_route_noalloc(const void* q, const void* k, const crisp_cfg* 
  * which calls that can overlap must not share: calls on one stream may, two
  * captured graphs only when they never run at the same time. out may be q
  * itself (address and strides); else out and score overlap no other tensor of
- * the call. The tensors' device has to be the current one. A kv_len outside [0, n_k] is clamped
- * and reported by crisp_cache_device_status as CRISP_ERR_INVALID_ARG. */
+ * the call. The tensors' device has to be the current one. A kv_len outside
+ * [0, n_k] is clamped and reported by crisp_cache_device_status as
+ * CRISP_ERR_INVALID_ARG. */
 
 typedef struct {
   int64_t seq, head, token; /* in elements; all three 0: contiguous in the order given above */

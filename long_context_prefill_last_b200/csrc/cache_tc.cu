@@ -38,8 +38,8 @@
 // maximum and the stores) and its two products follow one another. The start
 // and end of a job (set-up, first loads, the drained output) come on top: over
 // a launch of 8192 tokens the tensor pipe is busy 52% of the SMs' active
-// cycles, and the SMs are active 90% of the time. Starting the exponentials before the tile's maximum is known was slower (2.49 ms: the
-// registers spill).
+// cycles, and the SMs are active 90% of the time. Starting the exponentials
+// before the tile's maximum is known was slower (2.49 ms: the registers spill).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
@@ -190,8 +190,8 @@ __device__ __forceinline__ void soft_tile(SoftRow& st, uint32_t s_col, uint32_t 
     st.m_ref = tmax;
   }
   const float neg_m = st.m_ref == -INFINITY ? 0.f : -st.m_ref;
-  // P = 2^(x - m), rounded to bf16 for the product with V (l keeps it in
-  // fp32); chunk c0 goes to S columns [c0/2, c0/2 + 16), already consumed
+  // P = 2^(x - m), rounded to bf16, the type of V, for their product (a second
+  // one with the remainders would cost half as much again; l keeps fp32); chunk c0 goes to S columns [c0/2, c0/2 + 16), already consumed
   const uint64_t scale2 = dev::f2_pack(sl2, sl2), negm2 = dev::f2_pack(neg_m, neg_m);
   uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
